@@ -65,8 +65,10 @@ typedef enum {
     SOFTMAX_ERR_UNSUPPORTED = 2,     /* no device, wrong architecture, or a forced
                                         path that cannot take this shape */
     SOFTMAX_ERR_CUDA = 3,            /* a CUDA runtime call or launch failed */
-    SOFTMAX_ERR_DEVICE_TIMEOUT = 4   /* a kernel gave up a bounded wait (see
+    SOFTMAX_ERR_DEVICE_TIMEOUT = 4,  /* a kernel gave up a bounded wait (see
                                         softmax_device_status) */
+    SOFTMAX_ERR_DEVICE_INDEX = 5     /* a kernel met an index that leads out of
+                                        its tensors (see softmax_device_status) */
 } softmax_status_t;
 
 /* Execution paths chosen by the row-to-CTA scheduler. */
@@ -227,6 +229,153 @@ int softmax_attention_forward(const void* q, const void* k, const void* v, void*
                               int64_t batch_heads, int64_t n_q, int64_t n_k, int64_t head_dim,
                               int dtype, const softmax_attention_options_t* options,
                               void* stream);
+
+/*
+ * Attention of a decoder that serves requests: keys and values held in a
+ * paged cache, prompts packed one behind the other, grouped heads.  Three
+ * calls: softmax_kv_append rotates new tokens' queries and keys by their
+ * positions and puts keys and values into the cache,
+ * softmax_attention_packed computes the attention of whole prompts,
+ * softmax_attention_decode that of one new token of each sequence over the
+ * cache.
+ *
+ * Shared by the three:
+ *  - dtype SOFTMAX_BF16 or SOFTMAX_F16 (SOFTMAX_F32: SOFTMAX_ERR_UNSUPPORTED,
+ *    as for softmax_attention_forward); head_dim 64 or 128.
+ *  - Grouped heads: n_heads is a multiple of n_kv_heads, and query head h
+ *    reads key/value head h / (n_heads / n_kv_heads).
+ *  - softmax_heads_t names a [rows][heads][head_dim] tensor whose head_dim
+ *    elements are contiguous: element d of head h of row r is
+ *    data[r * row_stride + h * head_stride + d] (strides in ELEMENTS, so the
+ *    q, k and v parts of one projection's output are three of these).  data
+ *    and both strides are multiples of 16 bytes; strides are >= 0, and those
+ *    of an output give each of its rows' heads a place of its own.
+ *  - Index arrays (int32_t) are device memory and are read on the device:
+ *    their values are not known to the call.  A value that leads out of the
+ *    cache or of the tensors is not followed; what each call writes instead
+ *    is said there, and softmax_device_status then reports
+ *    SOFTMAX_ERR_DEVICE_INDEX.
+ *  - Ownership, asynchrony and errors as for softmax_attention_forward: one
+ *    kernel or two are queued on `stream`, nothing is launched when the
+ *    status is not SOFTMAX_OK.  The calls may be captured into graphs.
+ */
+typedef struct {
+    void* data;
+    int64_t row_stride, head_stride;
+} softmax_heads_t;
+
+/*
+ * A paged cache of keys and values.  Row r of page p holds one token: its
+ * head h is k[p * k_page_stride + r * k_row_stride + h * k_head_stride ...]
+ * (elements; multiples of 16 bytes), and likewise v.  Token position t of
+ * sequence s lies in page page_table[s * table_stride + t / page_size], row
+ * t mod page_size.  k and v may be parts of one allocation; each token's
+ * heads must have places of their own.  n_pages: entries of the table
+ * outside [0, n_pages) are bad (see above); entries of pages that a call
+ * does not reach are not read.  table_width * page_size <= 2^30.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t n_pages, page_size, n_kv_heads, head_dim;
+    int64_t k_page_stride, k_row_stride, k_head_stride;
+    int64_t v_page_stride, v_row_stride, v_head_stride;
+    const int32_t* page_table;
+    int64_t n_seqs, table_width, table_stride;
+} softmax_paged_cache_t;
+
+/*
+ * softmax_kv_append: for each token t < n_tokens, at position pos =
+ * positions[t] of sequence seq_ids[t] (NULL: t):
+ *     cache.k[pos] = rotate(k[t], pos), cache.v[pos] = v[t],
+ *     q_out[t] = rotate(q[t], pos)       (when q is given).
+ * rotate turns each pair (a, b) of a head's first rot_dim elements by the
+ * angle pos * inv_freq[i], i < rot_dim / 2: (a cos - b sin, a sin + b cos);
+ * elements past rot_dim are copied.  The pairs are (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when interleaved.  The angle is reduced modulo a full turn in
+ * 64-bit fixed point, so far positions lose nothing; the rotation is fp32,
+ * rounded once.
+ *
+ *   q, q_out   both NULL, or both given (n_heads heads); q_out may be q with
+ *              the same strides, and must not otherwise share bytes with q,
+ *              k or v (parts of one row layout are fine).  k, v and q must
+ *              not share bytes with the cache.
+ *   inv_freq   rot_dim / 2 doubles in device memory, radians per position;
+ *              rot_dim a multiple of 16, at most head_dim.  rot_dim 0 (inv_freq
+ *              then may be NULL): nothing is turned.
+ *   positions[t] < 0 marks padding: nothing of that token is written.  A
+ *   sequence outside [0, n_seqs), a position past the table or a bad page:
+ *   the token's key and value are not written (SOFTMAX_ERR_DEVICE_INDEX).
+ *   Two tokens at the same place: either's values remain, in any mixture.
+ *   n_tokens == 0: no-op.
+ */
+int softmax_kv_append(const softmax_paged_cache_t* cache, const softmax_heads_t* k,
+                      const softmax_heads_t* v, const softmax_heads_t* q,
+                      const softmax_heads_t* q_out, int64_t n_heads, const int32_t* positions,
+                      const int32_t* seq_ids, int64_t n_tokens, const double* inv_freq,
+                      int64_t rot_dim, int interleaved, int dtype, void* stream);
+
+/*
+ * softmax_attention_decode: one query row per sequence, over the first
+ * lengths[s] tokens of the sequence's cache:
+ *     o[s][h] = sum_t p_t v[t],  p = softmax over t < lengths[s] of
+ *               scale * (q[s][h] . k[t]).
+ * Scores, softmax and sums are fp32.  What lies in the cache at and past
+ * lengths[s] is not used.
+ *
+ *   q, o       [n_seqs][n_heads][head_dim]; o may be q with the same strides,
+ *              and must not otherwise share bytes with q.
+ *   lse        optional dense [n_seqs][n_heads] floats: natural-log
+ *              logsumexp of the scaled scores.
+ *   lengths    int32, n_seqs of them.  Length 0 gives NaN outputs (the
+ *              softmax of only -inf) and lse = -inf.  A negative length or
+ *              one past the table, and a bad page among a sequence's pages,
+ *              give NaN outputs for it (SOFTMAX_ERR_DEVICE_INDEX).
+ *   scale      0 < scale <= 2^127.
+ *   workspace  device memory of at least softmax_attention_decode_workspace
+ *              bytes, 16-byte aligned, contents of no matter before and
+ *              after.  The call uses it until its kernels have ended: calls
+ *              that may run at the same time need one each.
+ */
+int softmax_attention_decode(const softmax_paged_cache_t* cache, const softmax_heads_t* q,
+                             const softmax_heads_t* o, float* lse, int64_t n_heads,
+                             const int32_t* lengths, float scale, int dtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that softmax_attention_decode needs on the current
+ * device for these sizes (capacity: table_width * page_size); 0 is a valid
+ * answer, -1 says that a size is invalid or that there is no usable device. */
+int64_t softmax_attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads,
+                                           int64_t head_dim, int64_t capacity);
+
+/*
+ * softmax_attention_packed: attention of n_seqs sequences packed one behind
+ * the other.  Sequence s has the query rows [cu_q[s], cu_q[s + 1]) of q and
+ * the key rows [cu_k[s], cu_k[s + 1]) of k and v; for its query i, head h:
+ *     o[i][h] = sum_j p_j v[j],  p = softmax over visible j of
+ *               scale * (q[i][h] . k[j]).
+ * Every key of the sequence is visible, or with causal those with
+ * j <= i + (n_k - n_q) (i, j counted within the sequence: the last query
+ * sees every key).
+ *
+ *   q, o       [total_q][n_heads][head_dim], k, v [total_k][n_kv_heads]
+ *              [head_dim]; o may be q with the same strides, and must not
+ *              otherwise share bytes with q, k or v.
+ *   lse        optional dense [total_q][n_heads] floats.
+ *   cu_q, cu_k n_seqs + 1 int32 each, rising (cu_k may be cu_q).  A sequence
+ *              whose bounds fall or leave [0, total] is skipped
+ *              (SOFTMAX_ERR_DEVICE_INDEX).  Rows of o in no sequence are left
+ *              as they were.
+ *   A query that sees no key gives NaN (lse = -inf).  Values that a query
+ *   does not see have no influence on it, whatever they hold.
+ *   total_q and total_k below 2^31.
+ */
+int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
+                             const softmax_heads_t* v, const softmax_heads_t* o, float* lse,
+                             const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
+                             int64_t total_q, int64_t total_k, int64_t n_heads,
+                             int64_t n_kv_heads, int64_t head_dim, float scale, int causal,
+                             int dtype, void* stream);
 
 /*
  * softmax_strided: the softmax of rows whose elements are not contiguous.
@@ -423,9 +572,10 @@ int softmax_plan_describe(int64_t n_rows, int64_t n_cols, int dtype, char* buf, 
 /*
  * softmax_device_status: synchronises the current device, then reports
  * whether any kernel of this library gave up a bounded wait (an mbarrier that
- * never completed) since the last clear.  Returns SOFTMAX_OK or
- * SOFTMAX_ERR_DEVICE_TIMEOUT (SOFTMAX_ERR_CUDA if synchronisation fails).
- * clear != 0 resets the flag.
+ * never completed) or met a bad index (a page, sequence, length or row bound
+ * that leads out of its tensors) since the last clear.  Returns SOFTMAX_OK,
+ * SOFTMAX_ERR_DEVICE_TIMEOUT, else SOFTMAX_ERR_DEVICE_INDEX
+ * (SOFTMAX_ERR_CUDA if synchronisation fails).  clear != 0 resets both.
  */
 int softmax_device_status(int clear);
 

@@ -6,6 +6,8 @@ CUDA kernels.  The names mirror the C ABI in include/softmax.h:
     softmax_rows(x, out=None, stream=None, path=None)  torch tensors (CUDA)
     softmax_rows_ptr(...)                               raw pointers, C ABI call
     softmax_rows_host(h_in, h_out, d_in, d_out, ...)    host buffers, staged
+    kv_append(...), attention_packed(...), attention_decode(...)
+                                                        paged cache, packed prompts
     plan(...), plan_for_device(desc, ...)               scheduler decision
     device_status(clear), launch_count(), abi_version()
 
@@ -20,10 +22,12 @@ import os
 __all__ = [
     "F32", "BF16", "F16", "PATH_AUTO", "PATH_WARP", "PATH_CTA", "PATH_CLUSTER", "PATH_TWOPASS",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_CUDA", "ERR_DEVICE_TIMEOUT",
+    "ERR_DEVICE_INDEX",
     "SoftmaxError", "DeviceDesc", "Plan", "build", "lib", "library_path",
     "softmax_rows", "softmax_rows_ptr", "softmax_rows_ex_ptr", "softmax_rows_planned_ptr",
     "visible_cols", "softmax_backward", "softmax_backward_rows_ptr", "softmax",
     "softmax_strided_ptr", "attention", "attention_forward_ptr", "AttentionOptions",
+    "kv_append", "attention_packed", "attention_decode",
     "ATT_AUTO", "ATT_MMA", "ATT_TCGEN05", "ATT_TCGEN05_PINGPONG",
     "Options", "softmax_rows_host", "plan", "plan_for_device",
     "status_string", "device_status", "launch_count", "selftest_wait_timeout", "abi_version", "GB300",
@@ -33,6 +37,7 @@ F32, BF16, F16 = 0, 1, 2
 PATH_AUTO, PATH_WARP, PATH_CTA, PATH_CLUSTER, PATH_TWOPASS = -1, 0, 1, 2, 3
 PATH_NAMES = {PATH_WARP: "warp", PATH_CTA: "cta", PATH_CLUSTER: "cluster", PATH_TWOPASS: "twopass"}
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_TIMEOUT = 0, 1, 2, 3, 4
+ERR_DEVICE_INDEX = 5
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsoftmax.so")
@@ -155,6 +160,15 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def __getattr__(name: str):
+    # The serving operators (which need torch) load on first use.
+    if name in ("kv_append", "attention_packed", "attention_decode"):
+        from . import serving
+        globals()[name] = getattr(serving, name)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
+
 def status_string(status: int) -> str:
     return lib().softmax_status_string(status).decode()
 
@@ -173,7 +187,8 @@ def launch_count() -> int:
 
 
 def device_status(clear: bool = True) -> int:
-    """Synchronise the device; OK or ERR_DEVICE_TIMEOUT if a kernel gave up a wait."""
+    """Synchronise the device; OK, ERR_DEVICE_TIMEOUT if a kernel gave up a wait, or
+    ERR_DEVICE_INDEX if one met an index outside its tensors."""
     return lib().softmax_device_status(1 if clear else 0)
 
 

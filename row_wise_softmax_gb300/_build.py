@@ -20,11 +20,13 @@ LIB = os.path.join(PKG, "libsoftmax.so")
 
 SOURCES = ["softmax_abi.cu", "plan.cpp", "warp_rows.cu", "tile_rows.cu", "row_slices.cu",
            "row_slices_options.cu", "twopass.cu", "stream_rows.cu", "backward_rows.cu",
-           "columns.cu", "columns_stream.cu", "attention_mma.cu", "attention_tc.cu"]
+           "columns.cu", "columns_stream.cu", "attention_mma.cu", "attention_tc.cu",
+           "serving_abi.cu", "kv_append.cu", "attention_decode.cu", "attention_packed.cu"]
 # Sources that include another source file.
 INCLUDED = {"row_slices_options.cu": ["row_slices.cu"]}
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "cluster_ring.cuh",
-                                            "tensor_map.h", "attention_pp.h")] + [
+                                            "tensor_map.h", "attention_pp.h", "tcgen05.cuh",
+                                            "mma_sync.cuh", "serving.h")] + [
     os.path.join(INCLUDE, "softmax.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -27,6 +27,7 @@
 // softmax of only -inf (its logsumexp is -inf).
 #include "common.cuh"
 #include "kernels.h"
+#include "mma_sync.cuh"
 
 #include <atomic>
 
@@ -37,65 +38,6 @@ namespace {
 constexpr int kAttBM = 64;          // queries per CTA
 constexpr int kAttBN = 64;          // keys per tile
 constexpr int kAttThreads = 128;    // 4 warps x 16 queries
-
-template <typename T> struct MmaType;
-template <> struct MmaType<BF16Bits> {
-    __device__ static __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1)
-    {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-template <> struct MmaType<F16Bits> {
-    __device__ static __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1)
-    {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-                     "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-};
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-
-// 16-byte global -> shared copy; src_bytes 0 fills the 16 bytes with zeros.
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int src_bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit()
-{
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all_groups()
-{
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-// Byte offset of 16-byte chunk `c` of row `r` in a tile of D-element rows,
-// chunks XOR-swizzled by the row's low 3 bits.
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int r, int c)
-{
-    return static_cast<uint32_t>(r * D * 2 + ((c ^ (r & 7)) << 4));
-}
 
 // Copy rows [row0, row0 + ROWS) of a [n][D] matrix into a swizzled tile;
 // rows past n are zero.

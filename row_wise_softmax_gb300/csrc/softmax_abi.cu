@@ -4,6 +4,7 @@
 // library allocates no memory.
 #include "attention_pp.h"
 #include "kernels.h"
+#include "serving.h"
 
 #include <cmath>
 
@@ -134,6 +135,12 @@ int launch_path(const Problem& p, const softmax_plan_t& plan, cudaStream_t s)
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
+bool usable_device()
+{
+    softmax_device_desc_t d;
+    return current_device(&d) == SOFTMAX_OK && d.cc_major == 10 && d.cc_minor == 3;
+}
+
 int sm_count_current()
 {
     softmax_device_desc_t d;
@@ -182,6 +189,7 @@ const char* softmax_status_string(int status)
     case SOFTMAX_ERR_UNSUPPORTED: return "unsupported device or shape";
     case SOFTMAX_ERR_CUDA: return "CUDA error";
     case SOFTMAX_ERR_DEVICE_TIMEOUT: return "kernel gave up a bounded wait";
+    case SOFTMAX_ERR_DEVICE_INDEX: return "kernel met an index outside its tensors";
     default: return "unknown status";
     }
 }
@@ -639,8 +647,13 @@ int softmax_device_status(int clear)
                        rwsm::read_error_tile_rows(clear != 0) |
                        rwsm::read_error_stream_rows(clear != 0) |
                        rwsm::read_error_columns_stream(clear != 0) |
-                       rwsm::read_error_attention_tc(clear != 0);
-    return e ? SOFTMAX_ERR_DEVICE_TIMEOUT : SOFTMAX_OK;
+                       rwsm::read_error_attention_tc(clear != 0) |
+                       rwsm::read_error_kv_append(clear != 0) |
+                       rwsm::read_error_attention_decode(clear != 0) |
+                       rwsm::read_error_attention_packed(clear != 0);
+    if (e & ~static_cast<unsigned>(rwsm::kErrBadIndex))
+        return SOFTMAX_ERR_DEVICE_TIMEOUT;
+    return e ? SOFTMAX_ERR_DEVICE_INDEX : SOFTMAX_OK;
 }
 
 }  // extern "C"
