@@ -26,7 +26,7 @@ SOURCES = ["softmax_abi.cu", "plan.cpp", "warp_rows.cu", "tile_rows.cu", "row_sl
 INCLUDED = {"row_slices_options.cu": ["row_slices.cu"]}
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "kernels.h", "cluster_ring.cuh",
                                             "tensor_map.h", "attention_pp.h", "tcgen05.cuh",
-                                            "mma_sync.cuh", "serving.h")] + [
+                                            "mma_sync.cuh", "cta_pair.cuh", "serving.h")] + [
     os.path.join(INCLUDE, "softmax.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

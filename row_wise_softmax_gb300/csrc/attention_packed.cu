@@ -2,8 +2,13 @@
 //
 // This form: a warp per (query, head) row, walking the visible keys one at a
 // time with the running (m, l) softmax in fp32.
+#include "cluster_ring.cuh"
 #include "common.cuh"
 #include "serving.h"
+#include "tensor_map.h"
+#include "cta_pair.cuh"
+
+#include <atomic>
 
 namespace rwsm {
 
@@ -75,12 +80,38 @@ __device__ void attend_row(const PackedProblem& p, const unsigned short* q,
     }
 }
 
+// attend_row for query row `qrow`, head `head` over keys k0 .. k0 + n - 1, and
+// its output and logsumexp.
+template <typename T, int D>
+__device__ __forceinline__ void attend_row_store(const PackedProblem& p, int64_t qrow, int head,
+                                              int kvh, int64_t k0, int64_t n, float scale_log2)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float o[E], m, l;
+    attend_row<T, D>(
+        p, static_cast<const unsigned short*>(p.q.data) + qrow * p.q.row + head * p.q.head,
+        static_cast<const unsigned short*>(p.k.data) + k0 * p.k.row + kvh * p.k.head,
+        static_cast<const unsigned short*>(p.v.data) + k0 * p.v.row + kvh * p.v.head, n,
+        scale_log2, o, m, l);
+    const float inv = 1.0f / l;
+    unsigned short* dst =
+        static_cast<unsigned short*>(p.o.data) + qrow * p.o.row + head * p.o.head + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<unsigned*>(dst + e) = Elem<T>::pack2(o[e] * inv, o[e + 1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[qrow * p.n_heads + head] =
+            l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+// The form for operands that have no tensor map (repeated rows, no key at
+// all): a warp per (query, head) row.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 attention_packed_rows_kernel(const PackedProblem p, float scale_log2)
 {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
     const int head = blockIdx.y;
     const int kvh = head / (p.n_heads / p.n_kv_heads);
     pdl_launch_dependents();
@@ -104,33 +135,707 @@ attention_packed_rows_kernel(const PackedProblem p, float scale_log2)
                 break;
             int64_t n = p.causal ? i + n_k - n_q + 1 : n_k;
             n = n < 0 ? 0 : n;
-            float o[E], m, l;
-            attend_row<T, D>(
-                p, static_cast<const unsigned short*>(p.q.data) + (q0 + i) * p.q.row + head * p.q.head,
-                static_cast<const unsigned short*>(p.k.data) + k0 * p.k.row + kvh * p.k.head,
-                static_cast<const unsigned short*>(p.v.data) + k0 * p.v.row + kvh * p.v.head, n,
-                scale_log2, o, m, l);
-            const float inv = 1.0f / l;
-            unsigned short* dst = static_cast<unsigned short*>(p.o.data) + (q0 + i) * p.o.row +
-                                  head * p.o.head + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<unsigned*>(dst + e) = Elem<T>::pack2(o[e] * inv, o[e + 1] * inv);
-            if (p.lse && lane == 0)
-                p.lse[(q0 + i) * p.n_heads + head] =
-                    l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+            attend_row_store<T, D>(p, q0 + i, head, kvh, k0, n, scale_log2);
         }
         return;
     }
 }
 
-template <typename T, int D>
-cudaError_t launch(const PackedProblem& p, cudaStream_t s)
+// ------------------------------------------------------- the tensor core kernel
+constexpr int kBM = 128;                           // rows of a query tile (TMEM lanes)
+constexpr float kLazyRescaleLog2 = 8.0f;           // p <= 2^8 between rescales
+constexpr float kInf = __builtin_inff();
+
+// CTAs that share each product, keys per tile, warps that share a row of S,
+// ring slots of K and of V, CTAs per SM.
+template <int D> struct Shape;
+template <> struct Shape<128> {
+    static constexpr int CG = 2, BN = 128, HS = 2, KVS = 4, CTAS = 1;
+};
+template <> struct Shape<64> {
+    static constexpr int CG = 1, BN = 64, HS = 1, KVS = 4, CTAS = 2;
+};
+
+template <int D>
+constexpr int packed_threads()
 {
+    return 2 * 4 * Shape<D>::HS * 32 + 64;         // softmax warps, MMA warp, copy warp
+}
+
+template <int D>
+constexpr int packed_smem()
+{
+    using S = Shape<D>;
+    return (2 * kBM * D + 2 * S::KVS * (S::BN / S::CG) * D) * 2 + 1024;
+}
+
+// The unit of work of a CTA (pair): `tokens` query tokens of one sequence,
+// for the GP heads of one block.
+struct Unit {
+    int32_t q0, n_q, k0, n_k;
+    int32_t tile, head;                            // head: first of the block
+    int32_t ok;
+};
+
+// Number of sequence s's units that visit at least x key tiles (x >= 1), and
+// through `first` the first of them.
+__device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int32_t tokens, int bn,
+                                              bool causal, int32_t x, int32_t& first)
+{
+    const int32_t units = (n_q + tokens - 1) / tokens;
+    first = 0;
+    if (x <= 0)
+        return units;
+    if (units == 0 || x > (n_k + bn - 1) / bn)
+        return 0;
+    if (causal) {
+        // Unit i's last query min((i + 1) tokens, n_q) - 1 sees key (x - 1) bn.
+        const int64_t need = static_cast<int64_t>(x - 1) * bn - (n_k - n_q) + 1;
+        if (need > tokens)
+            first = static_cast<int32_t>((need + tokens - 1) / tokens) - 1;
+        if (first > units - 1)
+            first = units - 1;
+    }
+    return units - first;
+}
+
+// Unit number `rank` in the order in which units are handed out, by a warp:
+// the units that visit most key tiles first, so that the ones dispatched last
+// are short (above kRanked sequences: the order of the sequences).
+constexpr int kRanked = 128;
+
+__device__ Unit find_unit(const PackedProblem& p, int64_t rank, int32_t tokens, int bn, bool report)
+{
+    const int lane = threadIdx.x & 31;
+    Unit u = {};
+    auto lengths = [&](int64_t s, int32_t& q0, int32_t& n_q, int32_t& k0, int32_t& n_k) {
+        int64_t a = 0, b = 0, c = 0, d = 0;
+        if (s < p.n_seqs && !sequence_of(p, s, a, b, c, d) && report)
+            atomicOr(&g_error_attention_packed, kErrBadIndex);
+        q0 = static_cast<int32_t>(a);
+        n_q = static_cast<int32_t>(b);
+        k0 = static_cast<int32_t>(c);
+        n_k = static_cast<int32_t>(d);
+    };
+    auto sum = [](int64_t v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    int32_t q0, n_q, k0, n_k, first;
+    const bool ranked = p.n_seqs <= kRanked;
+    int32_t level = 0;                             // key tiles of the unit sought
+    int64_t above = 0;                             // units of higher levels
+    if (ranked) {
+        int32_t most = 0;
+        for (int64_t s = lane; s < p.n_seqs; s += 32) {
+            lengths(s, q0, n_q, k0, n_k);
+            most = n_q > 0 ? max(most, (n_k + bn - 1) / bn) : most;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        int32_t lo = 0, hi = most + 1;             // N(lo) > rank >= N(hi)
+        for (int pass = 0; lo + 1 < hi || pass == 0; ++pass) {
+            // The first pass asks for level 0: all units.
+            const int32_t x = pass == 0 ? 0 : lo + (hi - lo) / 2;
+            int64_t n = 0;
+            for (int64_t s = lane; s < p.n_seqs; s += 32) {
+                lengths(s, q0, n_q, k0, n_k);
+                n += units_with(n_q, n_k, tokens, bn, p.causal, x, first);
+            }
+            n = sum(n);
+            if (pass == 0) {
+                if (n <= rank)
+                    return u;
+            } else if (n > rank) {
+                lo = x;
+            } else {
+                hi = x;
+                above = n;
+            }
+        }
+        level = lo;
+    }
+    int64_t left = rank - above;
+    for (int64_t s0 = 0; s0 < p.n_seqs; s0 += 32) {
+        lengths(s0 + lane, q0, n_q, k0, n_k);
+        int32_t next, n = units_with(n_q, n_k, tokens, bn, p.causal, ranked ? level : 0, first);
+        const int32_t end = first + n;
+        if (ranked)
+            n -= units_with(n_q, n_k, tokens, bn, p.causal, level + 1, next);
+        int64_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += up;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > left);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            // Longest first within the sequence when units are not ranked.
+            const int32_t i = static_cast<int32_t>(left - (upto - n));
+            const int32_t tile = ranked ? first + i : end - 1 - i;
+            u.q0 = __shfl_sync(0xffffffffu, q0, at);
+            u.n_q = __shfl_sync(0xffffffffu, n_q, at);
+            u.k0 = __shfl_sync(0xffffffffu, k0, at);
+            u.n_k = __shfl_sync(0xffffffffu, n_k, at);
+            u.tile = __shfl_sync(0xffffffffu, tile, at);
+            u.ok = 1;
+            return u;
+        }
+        left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return u;
+}
+
+template <typename T, int D, bool CAUSAL>
+__global__ void __launch_bounds__(packed_threads<D>(), Shape<D>::CTAS)
+attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2)
+{
+    using S = Shape<D>;
+    constexpr int CG = S::CG, BN = S::BN, HS = S::HS, KVS = S::KVS;
+    constexpr bool kBF16 = Elem<T>::kNegInfBits == 0xff80u;
+    constexpr uint32_t QT_BYTES = kBM * D * 2;               // a query tile
+    constexpr uint32_t KV_BYTES = BN / CG * D * 2;           // this CTA's part of a key tile
+    constexpr int KR = BN / CG;                              // K rows of this CTA's part
+    constexpr int VD = D / CG;                               // V columns of this CTA's part
+    static_assert(VD == 64, "a V part is one 128-byte swizzle atom wide");
+    constexpr uint32_t IDESC_S = umma_idesc(kBM * CG, BN, kBF16, false);
+    constexpr uint32_t IDESC_PV = umma_idesc(kBM * CG, D, kBF16, true);
+    constexpr uint32_t TMEM_COLS = 2 * BN + 2 * D <= 256 ? 256u : 512u;
+    constexpr int CW = BN / HS;                              // keys of S per softmax warp
+    constexpr int NCH = CW / 32;                             // 32-column chunks per warp
+    static_assert(NCH == 2, "P arrives in two parts");
+    constexpr int OW = D / HS;                               // O columns per softmax warp
+    constexpr int CTRL = 2 * 4 * HS, LOADW = CTRL + 1;       // MMA warp, copy warp
+    extern __shared__ __align__(128) unsigned char pk_smem[];
+    __shared__ __align__(8) unsigned long long bar_s[2], bar_p[2][NCH], bar_fin[2], bar_drain;
+    __shared__ __align__(8) unsigned long long q_full, k_full[KVS], v_full[KVS];
+    __shared__ __align__(8) unsigned long long k_free[KVS], v_free[KVS];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int s_failed;
+    __shared__ Unit s_unit;
+    // Row maxima (by tile parity) and final sums of the warps sharing a row.
+    __shared__ float xmax[HS > 1 ? 2 : 1][2][HS][kBM];
+    __shared__ float xsum[2][HS][kBM];
+    __shared__ unsigned xredo[2][HS][4];
+
+    const uint32_t base = (smem_addr(pk_smem) + 1023u) & ~1023u;   // swizzle atoms
+    const uint32_t sQ = base, sK = sQ + 2 * QT_BYTES, sV = sK + KVS * KV_BYTES;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cta_rank<CG>();
+    const int gp = 1 << gp_log2;
+    const int tile_tokens = kBM >> gp_log2;                  // tokens of a query tile
+    const int tokens = 2 * CG * tile_tokens;                 // of the unit
+
+    if (warp == CTRL)
+        tmem_alloc_group<CG>(smem_addr(&tmem_slot), TMEM_COLS);
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_addr(&bar_s[x]), 1);
+            for (int c = 0; c < NCH; ++c)
+                mbar_init(smem_addr(&bar_p[x][c]), 4 * HS * CG);
+            mbar_init(smem_addr(&bar_fin[x]), 1);
+        }
+        mbar_init(smem_addr(&bar_drain), 1);
+        mbar_init(smem_addr(&q_full), 1);
+        for (int x = 0; x < KVS; ++x) {
+            mbar_init(smem_addr(&k_full[x]), 1);
+            mbar_init(smem_addr(&v_full[x]), 1);
+            mbar_init(smem_addr(&k_free[x]), 1);
+            mbar_init(smem_addr(&v_free[x]), 1);
+        }
+        s_failed = 0;
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == LOADW) {
+        const int64_t blocks = p.n_heads >> gp_log2;
+        const int64_t unit = blockIdx.x / CG;
+        Unit u = find_unit(p, unit / blocks, tokens, BN, unit == 0 && rank == 0);
+        u.head = static_cast<int32_t>(unit % blocks) << gp_log2;
+        if (lane == 0)
+            s_unit = u;
+    }
+    tc_fence_before();
+    group_sync<CG>();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Unit u = s_unit;
+    const int kvh = u.head / (p.n_heads / p.n_kv_heads);
+    const int32_t off = u.n_k - u.n_q;
+    // Key tiles that query tile x visits (both CTAs' parts of it), -1 when it
+    // has no tokens at all.
+    auto tiles_of = [&](int x) -> int32_t {
+        const int32_t begin = u.tile * tokens + x * CG * tile_tokens;
+        if (!u.ok || begin >= u.n_q)
+            return -1;
+        int32_t lim = u.n_k;
+        if (CAUSAL) {
+            const int32_t end = min(begin + CG * tile_tokens, u.n_q);
+            lim = min(lim, end + off);
+        }
+        return lim <= 0 ? 0 : (lim + BN - 1) / BN;
+    };
+    const int32_t nt[2] = {tiles_of(0), tiles_of(1)};
+    const int32_t n_kt = max(max(nt[0], nt[1]), 0);
+
+    auto slot = [](int32_t t) { return static_cast<uint32_t>(t) % KVS; };
+    auto phase = [](int32_t t) { return (static_cast<uint32_t>(t) / KVS) & 1u; };
+    auto fail = [&] { *reinterpret_cast<volatile int*>(&s_failed) = 1; };
+    auto failed_elsewhere = [&] { return *reinterpret_cast<volatile int*>(&s_failed) != 0; };
+    if (warp == LOADW) {
+        // --------------------------------------------------------- copy warp
+        // Each CTA copies its own query tiles, its rows of K and its columns
+        // of V; all complete on the even CTA's barriers, whose copy lane
+        // announces the bytes of both.
+        if (lane == 0 && n_kt > 0) {
+            bool failed = false;
+            auto wait1 = [&](uint32_t bar, uint32_t parity) {
+                if (!failed && !mbar_wait_group<CG>(bar, parity)) {
+                    failed = true;
+                    fail();
+                }
+            };
+            auto announce = [&](unsigned long long* bar, uint32_t bytes) {
+                if (rank == 0)
+                    mbar_arrive_expect_tx(smem_addr(bar), bytes * CG);
+                return leader_addr<CG>(smem_addr(bar));
+            };
+            int32_t k_issued = 0, v_issued = 0;
+            auto load_k = [&](int32_t t) {
+                const uint32_t bar = announce(&k_full[slot(t)], KV_BYTES);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d<CG>(sK + slot(t) * KV_BYTES + c * (KR * 128), &map_k, c * 64, kvh,
+                                    u.k0 + t * BN + static_cast<int>(rank) * KR, bar);
+                k_issued = t + 1;
+            };
+            auto load_v = [&](int32_t t) {
+                const uint32_t bar = announce(&v_full[slot(t)], KV_BYTES);
+                tma_load_3d<CG>(sV + slot(t) * KV_BYTES, &map_v, static_cast<int>(rank) * VD, kvh,
+                                u.k0 + t * BN, bar);
+                v_issued = t + 1;
+            };
+            const uint32_t bar_q = announce(&q_full, 2 * QT_BYTES);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d<CG>(sQ + x * QT_BYTES + c * (kBM * 128), &map_q, c * 64, u.head,
+                                    u.q0 + u.tile * tokens +
+                                        (x * CG + static_cast<int>(rank)) * tile_tokens, bar_q);
+            for (int32_t t = 0; t < KVS && t < n_kt; ++t) {
+                load_k(t);
+                load_v(t);
+            }
+            for (int32_t t = 0; t + KVS < n_kt && !failed; ++t) {
+                wait1(smem_addr(&k_free[slot(t)]), phase(t));      // every S(t) done
+                if (failed || failed_elsewhere())
+                    break;
+                load_k(t + KVS);
+                wait1(smem_addr(&v_free[slot(t)]), phase(t));      // every P V(t) done
+                if (failed || failed_elsewhere())
+                    break;
+                load_v(t + KVS);
+            }
+            if (rank == 0 && (failed || failed_elsewhere())) {
+                // Let the copies still in flight land (bounded; after one
+                // wait that ran out the others are not waited for).
+                bool ok = mbar_wait_group<CG>(smem_addr(&q_full), 0u);
+                for (int32_t t = k_issued > KVS ? k_issued - KVS : 0; t < k_issued && ok; ++t)
+                    ok = mbar_wait_group<CG>(smem_addr(&k_full[slot(t)]), phase(t));
+                for (int32_t t = v_issued > KVS ? v_issued - KVS : 0; t < v_issued && ok; ++t)
+                    ok = mbar_wait_group<CG>(smem_addr(&v_full[slot(t)]), phase(t));
+            }
+        }
+        __syncwarp();
+    } else if (warp == CTRL) {
+        // ---------------------------------------------------------- MMA warp
+        // Lane 0 of the even CTA issues every product.
+        if (lane == 0 && rank == 0 && n_kt > 0) {
+            bool failed = false;
+            auto wait1 = [&](uint32_t bar, uint32_t parity) {
+                if (!failed && !mbar_wait_group<CG>(bar, parity)) {
+                    failed = true;
+                    fail();
+                }
+            };
+            auto issue_s = [&](int x, int32_t t) {
+                const uint32_t cK = sK + slot(t) * KV_BYTES;
+                const uint32_t qx = sQ + static_cast<uint32_t>(x) * QT_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    umma_f16_group<CG>(
+                        tmem + static_cast<uint32_t>(x * BN),
+                        smem_desc_sw128(qx + (ks >> 2) * (kBM * 128) + (ks & 3) * 32, 16, 1024),
+                        smem_desc_sw128(cK + (ks >> 2) * (KR * 128) + (ks & 3) * 32, 16, 1024),
+                        IDESC_S, ks > 0 ? 1u : 0u);
+            };
+            // P_X (16-bit) lies over S_X: each softmax warp's CW keys in the
+            // first CW / 2 columns of its own part.  Part c of P is the c-th
+            // 32 keys of every warp.
+            auto issue_pv = [&](int x, int32_t t, int c) {
+                const uint32_t cV = sV + slot(t) * KV_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < BN / 16; ++ks)
+                    if ((ks * 16 % CW) / 32 == c)
+                        umma_f16_ta_group<CG>(
+                            tmem + static_cast<uint32_t>(2 * BN + x * D),
+                            tmem + static_cast<uint32_t>(x * BN + ks * 8 + (ks * 16 / CW) * (CW / 2)),
+                            smem_desc_sw128(cV + ks * 2048, 16, 1024), IDESC_PV,
+                            (t > 0 || ks > 0) ? 1u : 0u);
+            };
+            wait1(smem_addr(&q_full), 0u);
+            wait1(smem_addr(&k_full[0]), 0u);
+            if (!failed) {
+                tc_fence_after();
+                for (int x = 0; x < 2; ++x)
+                    if (nt[x] > 0) {
+                        issue_s(x, 0);
+                        umma_commit_group<CG>(smem_addr(&bar_s[x]));
+                    }
+                umma_commit_group<CG>(smem_addr(&k_free[0]));      // S(0) done
+            }
+            for (int32_t t = 0; t < n_kt && !failed; ++t) {
+                wait1(smem_addr(&v_full[slot(t)]), phase(t));
+                if (t + 1 < n_kt)
+                    wait1(smem_addr(&k_full[slot(t + 1)]), phase(t + 1));
+                for (int x = 0; x < 2 && !failed; ++x) {
+                    if (t >= nt[x])
+                        continue;
+                    for (int c = 0; c < NCH && !failed; ++c) {
+                        wait1(smem_addr(&bar_p[x][c]), static_cast<uint32_t>(t & 1));
+                        if (failed)
+                            break;
+                        tc_fence_after();
+                        issue_pv(x, t, c);
+                    }
+                    if (failed)
+                        break;
+                    if (x == 1 || t >= nt[1])                      // the last one of V(t)
+                        umma_commit_group<CG>(smem_addr(&v_free[slot(t)]));
+                    const bool more = t + 1 < nt[x];
+                    if (more) {
+                        issue_s(x, t + 1);
+                        if (x == 1 || t + 1 >= nt[1])              // the last one of K(t + 1)
+                            umma_commit_group<CG>(smem_addr(&k_free[slot(t + 1)]));
+                    }
+                    umma_commit_group<CG>(smem_addr(more ? &bar_s[x] : &bar_fin[x]));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- softmax warps
+        // Warp w: query tile x, TMEM lane group w % 4 (rows 32 (w % 4) ..),
+        // and part h of the tile's keys and of O's columns when HS warps
+        // share a row.
+        const int x = warp / (4 * HS), h = (warp / 4) % HS;
+        const int r = (warp & 3) * 32 + lane;                // row of the tile = TMEM lane
+        const int32_t first = u.tile * tokens + (x * CG + static_cast<int>(rank)) * tile_tokens;
+        const int32_t token = first + (r >> gp_log2);        // of the sequence
+        const int32_t head = u.head + (r & (gp - 1));
+        const bool real = u.ok && token < u.n_q;
+        // Keys visible to this row, and to every row of the tile.
+        const int32_t limit = CAUSAL ? min(u.n_k, token + off + 1) : u.n_k;
+        const int32_t limit_all = CAUSAL ? min(u.n_k, first + off + 1) : u.n_k;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_col = static_cast<uint32_t>(x * BN + h * CW);
+        const uint32_t o_col = static_cast<uint32_t>(2 * BN + x * D + h * OW);
+        const int pair_bar = 1 + x * 4 + (warp & 3);         // the HS warps of 32 rows
+        const int32_t my_kt = nt[x];
+        float m = kNegInf, l = 0.0f;                         // l: this warp's part of the sum
+        bool failed = false;                                 // warp-uniform
+        uint32_t bar_parts[NCH];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+            bar_parts[c] = leader_addr<CG>(smem_addr(&bar_p[x][c]));
+        for (int32_t t = 0; t < my_kt; ++t) {
+            const bool ok = failed || mbar_wait_bounded(smem_addr(&bar_s[x]),
+                                                        static_cast<uint32_t>(t & 1));
+            if (__any_sync(0xffffffffu, !ok) && !failed) {
+                failed = true;
+                fail();
+            }
+            tc_fence_after();
+            float sv[NCH][32];
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+                tmem_ld32(t_row + s_col + c * 32, sv[c]);
+            tmem_wait_ld();
+            if ((t + 1) * BN > limit_all) {                  // some row has a masked key
+                const int32_t keep = limit - t * BN - h * CW;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c * 32 + j >= keep)
+                            sv[c][j] = kNegInf;
+            }
+            float mx = kNegInf;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    mx = max3(mx, sv[c][j], sv[c][j + 1]);
+            if constexpr (HS > 1) {
+                const int par = t & 1;
+                xmax[par][x][h][r] = mx;
+                named_barrier(pair_bar, 32 * HS);
+#pragma unroll
+                for (int o = 0; o < HS; ++o)
+                    mx = fmaxf(mx, xmax[par][x][o][r]);
+            }
+            // Lazy rescaling: the reference m (base 2) moves only when the
+            // tile's max exceeds it by more than 2^8; O / l and the logsumexp
+            // only need m and l to agree.
+            const float mx_s = mx * scale_log2;
+            float alpha = 1.0f;
+            if (mx_s > m + kLazyRescaleLog2) {
+                alpha = ex2_ftz(m - mx_s);
+                m = mx_s;
+            }
+            const float nref = m == kNegInf ? 0.0f : -m;
+            if (t > 0 && !__all_sync(0xffffffffu, alpha == 1.0f)) {
+#pragma unroll 1
+                for (int c = 0; c < OW; c += 8)
+                    tmem_scale8(t_row + o_col + c, alpha);
+            }
+            float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float p0, p1;
+                    fma2(p0, p1, sv[c][2 * j], sv[c][2 * j + 1], scale_log2, scale_log2, nref, nref);
+                    p0 = ex2_ftz(p0);
+                    p1 = ex2_ftz(p1);
+                    add2(sum0, sum1, sum0, sum1, p0, p1);
+                    w[j] = Elem<T>::pack2(p0, p1);
+                }
+                tmem_st16(t_row + s_col + c * 16, w);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_leader<CG>(bar_parts[c]);    // release: O rescaled, this part of P
+            }
+            l = l * alpha + (sum0 + sum1);
+        }
+        if (my_kt > 0) {
+            const bool ok = failed || mbar_wait_bounded(smem_addr(&bar_fin[x]), 0u);
+            if (__any_sync(0xffffffffu, !ok) && !failed) {
+                failed = true;
+                fail();
+            }
+            tc_fence_after();
+        }
+        if constexpr (HS > 1) {
+            xsum[x][h][r] = l;
+            named_barrier(pair_bar, 32 * HS);
+            l = 0.0f;
+#pragma unroll
+            for (int o = 0; o < HS; ++o)
+                l += xsum[x][o][r];
+        }
+        if (!failed && my_kt >= 0) {
+            const float inv = 1.0f / l;
+            unsigned short* const dst = static_cast<unsigned short*>(p.o.data) +
+                                        (u.q0 + static_cast<int64_t>(token)) * p.o.row +
+                                        head * p.o.head + h * OW;
+            // A masked key's weight is 0, but 0 times an infinite or NaN
+            // value of V is NaN: rows that came out so, and have such a value
+            // in the masked part of their key tiles, are done again over
+            // their visible keys alone (by the row's first warp, and before
+            // anything is stored there: o may be q).
+            bool finite = true;
+            if (my_kt > 0) {                                 // warp-uniform, as tcgen05.ld needs
+#pragma unroll
+                for (int c = 0; c < OW / 32; ++c) {
+                    float ov[32];
+                    tmem_ld32(t_row + o_col + c * 32, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        finite = finite && fabsf(ov[j] * inv) < kInf;
+                }
+            }
+            unsigned redo = __ballot_sync(0xffffffffu, real && limit > 0 && !finite);
+            if constexpr (HS > 1) {
+                if (lane == 0)
+                    xredo[x][h][warp & 3] = redo;
+                named_barrier(pair_bar, 32 * HS);
+#pragma unroll
+                for (int o = 0; o < HS; ++o)
+                    redo |= xredo[x][o][warp & 3];
+            }
+            if (redo) {
+                const unsigned short* const v = static_cast<const unsigned short*>(p.v.data) +
+                                                static_cast<int64_t>(u.k0) * p.v.row +
+                                                kvh * p.v.head;
+                const int32_t from = __reduce_min_sync(0xffffffffu,
+                                                       redo >> lane & 1 ? limit : 0x7fffffff);
+                const int64_t to = min(static_cast<int64_t>(my_kt) * BN, p.total_k - u.k0);
+                bool hit = false;
+                for (int64_t i = static_cast<int64_t>(from) * (D / 2) + lane; i < to * (D / 2);
+                     i += 32) {
+                    float a, b;
+                    Elem<T>::unpack2(__ldg(reinterpret_cast<const unsigned*>(
+                                         v + (i / (D / 2)) * p.v.row + (i % (D / 2)) * 2)), a, b);
+                    hit = hit || !(fabsf(a) < kInf) || !(fabsf(b) < kInf);
+                }
+                if (!__any_sync(0xffffffffu, hit))
+                    redo = 0;
+            }
+            const bool store = real && !(redo >> lane & 1);
+            // A row that sees no key is the softmax of only -inf: NaN.
+            const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int c = 0; c < OW / 32; ++c) {
+                float ov[32];
+                if (my_kt > 0) {
+                    tmem_ld32(t_row + o_col + c * 32, ov);
+                    tmem_wait_ld();
+                }
+                if (store) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        ov[j] = limit > 0 ? ov[j] * inv : nan;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint4 w;
+                        w.x = Elem<T>::pack2(ov[g * 8 + 0], ov[g * 8 + 1]);
+                        w.y = Elem<T>::pack2(ov[g * 8 + 2], ov[g * 8 + 3]);
+                        w.z = Elem<T>::pack2(ov[g * 8 + 4], ov[g * 8 + 5]);
+                        w.w = Elem<T>::pack2(ov[g * 8 + 6], ov[g * 8 + 7]);
+                        *reinterpret_cast<uint4*>(dst + c * 32 + g * 8) = w;
+                    }
+                }
+            }
+            if (p.lse && store && h == 0)
+                p.lse[(u.q0 + static_cast<int64_t>(token)) * p.n_heads + head] =
+                    limit > 0 && l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
+            while (redo && h == 0) {
+                const int row = (warp & 3) * 32 + __ffs(redo) - 1;
+                redo &= redo - 1;
+                const int32_t tok = first + (row >> gp_log2);
+                attend_row_store<T, D>(p, u.q0 + static_cast<int64_t>(tok),
+                                       u.head + (row & (gp - 1)), kvh, u.k0,
+                                       CAUSAL ? min(u.n_k, tok + off + 1) : u.n_k, scale_log2);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == CTRL * 32 && failed_elsewhere()) {
+        atomicOr(&g_error_attention_packed, kErrMbarrierTimeout);
+        if (rank == 0) {
+            // One more commit: it arrives once every tensor core operation
+            // this thread has issued has completed; wait for it (bounded)
+            // before tensor memory is freed.
+            tc_fence_after();
+            umma_commit_group<CG>(smem_addr(&bar_drain));
+            mbar_wait_bounded(smem_addr(&bar_drain), 0u);
+        }
+    }
+    tc_fence_before();
+    group_sync<CG>();
+    if (warp == CTRL) {
+        tc_fence_after();
+        tmem_dealloc_group<CG>(tmem, TMEM_COLS);
+    }
+}
+
+// 3-D tensor map (element, head, row) of a [rows][heads][D] operand: boxes of
+// 64 elements (128 bytes, 128-byte swizzle) x box_heads x box_rows; rows past
+// the tensor's end read as zero.
+inline bool packed_tensor_map(CUtensorMap* map, const Heads& t, int64_t rows, int64_t heads, int d,
+                              int box_heads, int box_rows, int dtype)
+{
+    auto encode = tensor_map_encoder();
+    if (!encode)
+        return false;
+    // A stride that is never taken may be anything; one that repeats an
+    // element (0) or passes the map's 40 bits has no map.
+    const int64_t hs = heads > 1 ? t.head : d, rs = rows > 1 ? t.row : hs * heads;
+    if (hs < d || rs < d || hs >= (int64_t{1} << 38) || rs >= (int64_t{1} << 38))
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2,
+                                   static_cast<cuuint64_t>(rs) * 2};
+    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+                               static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estride[3] = {1u, 1u, 1u};
+    return encode(map, dtype == SOFTMAX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  3, t.data, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool CAUSAL>
+cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
+{
+    using S = Shape<D>;
+    // Query rows of a tile are tokens x heads of one group: as many heads as
+    // the largest power of two that divides the group.
+    const int group = p.n_heads / p.n_kv_heads;
+    int gp_log2 = 0;
+    while (gp_log2 < 5 && group % (2 << gp_log2) == 0)
+        ++gp_log2;
+    const int tile_tokens = kBM >> gp_log2, tokens = 2 * S::CG * tile_tokens;
+    const int64_t units = (p.total_q / tokens + p.n_seqs) * (p.n_heads >> gp_log2);
+    if (units * S::CG > 0x7fffffff)
+        return cudaErrorNotSupported;
+    CUtensorMap mq, mk, mv;
+    if (p.total_k == 0 ||
+        !packed_tensor_map(&mq, p.q, p.total_q, p.n_heads, D, 1 << gp_log2, tile_tokens, p.dtype) ||
+        !packed_tensor_map(&mk, p.k, p.total_k, p.n_kv_heads, D, 1, S::BN / S::CG, p.dtype) ||
+        !packed_tensor_map(&mv, p.v, p.total_k, p.n_kv_heads, D, 1, S::BN, p.dtype))
+        return cudaErrorNotSupported;                    // nothing launched
+    auto* kern = attention_packed_kernel<T, D, CAUSAL>;
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, packed_smem<D>());
+        if (e != cudaSuccess)
+            return e;
+        attr_set[dev].store(true);
+    }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.total_q / kTileTokens + p.n_seqs),
-                       static_cast<unsigned>(p.n_heads), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(units * S::CG), 1, 1);
+    cfg.blockDim = dim3(packed_threads<D>(), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(packed_smem<D>());
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, S::CG));
+    const float scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p, scale_log2, gp_log2);
+    note_launch();
+    return err;
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const PackedProblem& p, cudaStream_t s)
+{
+    const int64_t tiles = p.total_q / kTileTokens + p.n_seqs;
+    if (tiles > 0x7fffffff || p.n_heads > 65535)
+        return cudaErrorNotSupported;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(p.n_heads), 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
@@ -140,6 +845,14 @@ cudaError_t launch(const PackedProblem& p, cudaStream_t s)
                                                scale_log2);
     note_launch();
     return err;
+}
+
+template <typename T, int D>
+cudaError_t launch(const PackedProblem& p, cudaStream_t s)
+{
+    const cudaError_t err = p.causal ? launch_tiles<T, D, true>(p, s)
+                                     : launch_tiles<T, D, false>(p, s);
+    return err == cudaErrorNotSupported ? launch_rows<T, D>(p, s) : err;
 }
 
 }  // namespace
