@@ -397,7 +397,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         if (lane == 0 && n_kt > 0) {
             bool failed = false;
             auto wait1 = [&](uint32_t bar, uint32_t parity) {
-                if (!failed && !mbar_wait_group<CG>(bar, parity)) {
+                if (!failed && !mbar_wait_bounded(bar, parity)) {
                     failed = true;
                     fail();
                 }
@@ -447,86 +447,90 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             if (rank == 0 && (failed || failed_elsewhere())) {
                 // Let the copies still in flight land (bounded; after one
                 // wait that ran out the others are not waited for).
-                bool ok = mbar_wait_group<CG>(smem_addr(&q_full), 0u);
+                bool ok = mbar_wait_bounded(smem_addr(&q_full), 0u);
                 for (int32_t t = k_issued > KVS ? k_issued - KVS : 0; t < k_issued && ok; ++t)
-                    ok = mbar_wait_group<CG>(smem_addr(&k_full[slot(t)]), phase(t));
+                    ok = mbar_wait_bounded(smem_addr(&k_full[slot(t)]), phase(t));
                 for (int32_t t = v_issued > KVS ? v_issued - KVS : 0; t < v_issued && ok; ++t)
-                    ok = mbar_wait_group<CG>(smem_addr(&v_full[slot(t)]), phase(t));
+                    ok = mbar_wait_bounded(smem_addr(&v_full[slot(t)]), phase(t));
             }
         }
         __syncwarp();
     } else if (warp == CTRL) {
         // ---------------------------------------------------------- MMA warp
-        // Lane 0 of the even CTA issues every product.
-        if (lane == 0 && rank == 0 && n_kt > 0) {
+        // The even CTA's warp issues every product; it runs its loop as a
+        // whole warp (see umma_f16_warp).  A 16-element step of Q or K is 32
+        // bytes into the 128-byte atom row, of V (MN-major) 16 key rows.
+        if (rank == 0 && n_kt > 0) {
             bool failed = false;
             auto wait1 = [&](uint32_t bar, uint32_t parity) {
-                if (!failed && !mbar_wait_group<CG>(bar, parity)) {
+                if (!failed && __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity))) {
                     failed = true;
                     fail();
                 }
             };
-            auto issue_s = [&](int x, int32_t t) {
-                const uint32_t cK = sK + slot(t) * KV_BYTES;
-                const uint32_t qx = sQ + static_cast<uint32_t>(x) * QT_BYTES;
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(sK, 16, 1024), dv = smem_desc_sw128(sV, 16, 1024);
+            auto issue_s = [&](int x, uint32_t at) {
+                const uint64_t a = dq + x * (QT_BYTES >> 4), b = dk + at * (KV_BYTES >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    umma_f16_group<CG>(
-                        tmem + static_cast<uint32_t>(x * BN),
-                        smem_desc_sw128(qx + (ks >> 2) * (kBM * 128) + (ks & 3) * 32, 16, 1024),
-                        smem_desc_sw128(cK + (ks >> 2) * (KR * 128) + (ks & 3) * 32, 16, 1024),
-                        IDESC_S, ks > 0 ? 1u : 0u);
+                    umma_f16_warp<CG>(tmem + static_cast<uint32_t>(x * BN),
+                                      a + ((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16,
+                                      b + ((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16, IDESC_S,
+                                      ks > 0 ? 1u : 0u);
             };
             // P_X (16-bit) lies over S_X: each softmax warp's CW keys in the
             // first CW / 2 columns of its own part.  Part c of P is the c-th
             // 32 keys of every warp.
-            auto issue_pv = [&](int x, int32_t t, int c) {
-                const uint32_t cV = sV + slot(t) * KV_BYTES;
+            auto issue_pv = [&](int x, uint32_t at, int c, bool begin) {
+                const uint64_t b = dv + at * (KV_BYTES >> 4);
 #pragma unroll
                 for (int ks = 0; ks < BN / 16; ++ks)
                     if ((ks * 16 % CW) / 32 == c)
-                        umma_f16_ta_group<CG>(
+                        umma_f16_ta_warp<CG>(
                             tmem + static_cast<uint32_t>(2 * BN + x * D),
                             tmem + static_cast<uint32_t>(x * BN + ks * 8 + (ks * 16 / CW) * (CW / 2)),
-                            smem_desc_sw128(cV + ks * 2048, 16, 1024), IDESC_PV,
-                            (t > 0 || ks > 0) ? 1u : 0u);
+                            b + ks * (2048 / 16), IDESC_PV, begin && ks == 0 ? 0u : 1u);
             };
             wait1(smem_addr(&q_full), 0u);
             wait1(smem_addr(&k_full[0]), 0u);
             if (!failed) {
                 tc_fence_after();
+#pragma unroll
                 for (int x = 0; x < 2; ++x)
                     if (nt[x] > 0) {
                         issue_s(x, 0);
-                        umma_commit_group<CG>(smem_addr(&bar_s[x]));
+                        umma_commit_warp<CG>(smem_addr(&bar_s[x]));
                     }
-                umma_commit_group<CG>(smem_addr(&k_free[0]));      // S(0) done
+                umma_commit_warp<CG>(smem_addr(&k_free[0]));       // S(0) done
             }
             for (int32_t t = 0; t < n_kt && !failed; ++t) {
                 wait1(smem_addr(&v_full[slot(t)]), phase(t));
                 if (t + 1 < n_kt)
                     wait1(smem_addr(&k_full[slot(t + 1)]), phase(t + 1));
-                for (int x = 0; x < 2 && !failed; ++x) {
-                    if (t >= nt[x])
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (failed || t >= nt[x])
                         continue;
-                    for (int c = 0; c < NCH && !failed; ++c) {
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) {
                         wait1(smem_addr(&bar_p[x][c]), static_cast<uint32_t>(t & 1));
-                        if (failed)
-                            break;
-                        tc_fence_after();
-                        issue_pv(x, t, c);
+                        if (!failed) {
+                            tc_fence_after();
+                            issue_pv(x, slot(t), c, t == 0);
+                        }
                     }
                     if (failed)
-                        break;
+                        continue;
                     if (x == 1 || t >= nt[1])                      // the last one of V(t)
-                        umma_commit_group<CG>(smem_addr(&v_free[slot(t)]));
+                        umma_commit_warp<CG>(smem_addr(&v_free[slot(t)]));
                     const bool more = t + 1 < nt[x];
                     if (more) {
-                        issue_s(x, t + 1);
+                        issue_s(x, slot(t + 1));
                         if (x == 1 || t + 1 >= nt[1])              // the last one of K(t + 1)
-                            umma_commit_group<CG>(smem_addr(&k_free[slot(t + 1)]));
+                            umma_commit_warp<CG>(smem_addr(&k_free[slot(t + 1)]));
                     }
-                    umma_commit_group<CG>(smem_addr(more ? &bar_s[x] : &bar_fin[x]));
+                    umma_commit_warp<CG>(smem_addr(more ? &bar_s[x] : &bar_fin[x]));
                 }
             }
         }
@@ -734,16 +738,18 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == CTRL * 32 && failed_elsewhere()) {
-        atomicOr(&g_error_attention_packed, kErrMbarrierTimeout);
+    if (warp == CTRL && failed_elsewhere()) {
+        if (lane == 0)
+            atomicOr(&g_error_attention_packed, kErrMbarrierTimeout);
         if (rank == 0) {
             // One more commit: it arrives once every tensor core operation
-            // this thread has issued has completed; wait for it (bounded)
+            // this warp has issued has completed; wait for it (bounded)
             // before tensor memory is freed.
             tc_fence_after();
-            umma_commit_group<CG>(smem_addr(&bar_drain));
+            umma_commit_warp<CG>(smem_addr(&bar_drain));
             mbar_wait_bounded(smem_addr(&bar_drain), 0u);
         }
+        __syncwarp();
     }
     tc_fence_before();
     group_sync<CG>();

@@ -42,39 +42,18 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t addr)
     return r;
 }
 
+// Arrive on the even CTA's barrier.  What it announces lies in tensor memory
+// and is ordered by tcgen05.wait and tcgen05.fence before it; no other memory
+// is handed over, so the arrival and the waits keep the CTA scope (with
+// .release.cluster and .acquire.cluster each wait that was already over cost
+// about 250 cycles, each arrival several hundred).
 template <int CG>
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t addr)
 {
     if constexpr (CG == 1)
         mbar_arrive(addr);
     else
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                     :: "r"(addr) : "memory");
-}
-
-// mbar_wait_bounded for a phase that threads of the other CTA complete too.
-template <int CG>
-__device__ __forceinline__ bool mbar_wait_group(uint32_t bar, uint32_t parity)
-{
-    if constexpr (CG == 1)
-        return mbar_wait_bounded(bar, parity);
-    unsigned long long t0 = 0;
-    for (uint32_t it = 0; it < (1u << 30); ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (ok)
-            return true;
-        const unsigned long long now = global_ns();
-        if (it == 0)
-            t0 = now;
-        else if (now - t0 > kWaitLimitNs)
-            return false;
-    }
-    return false;
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
 template <int CG>
@@ -100,42 +79,61 @@ __device__ __forceinline__ void tmem_dealloc_group(uint32_t taddr, uint32_t ncol
                      :: "r"(taddr), "r"(ncols) : "memory");
 }
 
+// Products and commits, called by a whole warp in uniform control flow: the
+// instruction itself is executed by the lane that elect.sync picks (the same
+// one each time).  Their operands are warp-uniform registers, which uniform
+// code holds already; issued from inside a one-lane branch they were moved
+// there one by one, about 100 cycles a product beside busy warps.
 template <int CG>
-__device__ __forceinline__ void umma_f16_group(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void umma_f16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate)
 {
     if constexpr (CG == 1)
-        umma_f16(d_tmem, a_desc, b_desc, idesc, accumulate);
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                     : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                      : "memory");
 }
 
+// The same with A in tensor memory.
 template <int CG>
-__device__ __forceinline__ void umma_f16_ta_group(uint32_t d_tmem, uint32_t a_tmem,
-                                                  uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t accumulate)
+__device__ __forceinline__ void umma_f16_ta_warp(uint32_t d_tmem, uint32_t a_tmem,
+                                                 uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate)
 {
     if constexpr (CG == 1)
-        umma_f16_ta(d_tmem, a_tmem, b_desc, idesc, accumulate);
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                     :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                     : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                      :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                      : "memory");
 }
 
 // Commit to the barrier at this offset in both CTAs.
 template <int CG>
-__device__ __forceinline__ void umma_commit_group(uint32_t bar)
+__device__ __forceinline__ void umma_commit_warp(uint32_t bar)
 {
     if constexpr (CG == 1)
-        umma_commit(bar);
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+                     "[%0];\n\t}" :: "r"(bar) : "memory");
     else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
-                     ".multicast::cluster.b64 [%0], %1;"
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;\n\t}"
                      :: "r"(bar), "h"(static_cast<unsigned short>(3)) : "memory");
 }
 
