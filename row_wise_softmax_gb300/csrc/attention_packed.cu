@@ -159,7 +159,7 @@ template <> struct Shape<64> {
 template <int D>
 constexpr int packed_threads()
 {
-    return 2 * 4 * Shape<D>::HS * 32 + 64;         // softmax warps, MMA warp, copy warp
+    return 2 * 4 * Shape<D>::HS * 32 + 96;         // softmax warps, two MMA warps, copy warp
 }
 
 template <int D>
@@ -306,14 +306,16 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     static_assert(VD == 64, "a V part is one 128-byte swizzle atom wide");
     constexpr uint32_t IDESC_S = umma_idesc(kBM * CG, BN, kBF16, false);
     constexpr uint32_t IDESC_PV = umma_idesc(kBM * CG, D, kBF16, true);
-    constexpr uint32_t TMEM_COLS = 2 * BN + 2 * D <= 256 ? 256u : 512u;
+    // Tensor memory: S of either query tile (BN columns), P of each (BN / 2),
+    // O of each (D).
+    constexpr uint32_t P_COL = BN, O_COL = 2 * BN, TMEM_COLS = 2 * BN + 2 * D;
+    static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two");
     constexpr int CW = BN / HS;                              // keys of S per softmax warp
     constexpr int NCH = CW / 32;                             // 32-column chunks per warp
-    static_assert(NCH == 2, "P arrives in two parts");
     constexpr int OW = D / HS;                               // O columns per softmax warp
-    constexpr int CTRL = 2 * 4 * HS, LOADW = CTRL + 1;       // MMA warp, copy warp
+    constexpr int CTRL = 2 * 4 * HS, LOADW = CTRL + 2;       // MMA warps, copy warp
     extern __shared__ __align__(128) unsigned char pk_smem[];
-    __shared__ __align__(8) unsigned long long bar_s[2], bar_p[2][NCH], bar_fin[2], bar_drain;
+    __shared__ __align__(8) unsigned long long bar_s[2], bar_ld[2], bar_p[2], bar_pv[2], bar_drain[2];
     __shared__ __align__(8) unsigned long long q_full, k_full[KVS], v_full[KVS];
     __shared__ __align__(8) unsigned long long k_free[KVS], v_free[KVS];
     __shared__ uint32_t tmem_slot;
@@ -337,17 +339,17 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     if (tid == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_addr(&bar_s[x]), 1);
-            for (int c = 0; c < NCH; ++c)
-                mbar_init(smem_addr(&bar_p[x][c]), 4 * HS * CG);
-            mbar_init(smem_addr(&bar_fin[x]), 1);
+            mbar_init(smem_addr(&bar_p[x]), 4 * HS * CG);
+            mbar_init(smem_addr(&bar_ld[x]), 4 * HS * CG);
+            mbar_init(smem_addr(&bar_pv[x]), 1);
+            mbar_init(smem_addr(&bar_drain[x]), 1);
         }
-        mbar_init(smem_addr(&bar_drain), 1);
         mbar_init(smem_addr(&q_full), 1);
         for (int x = 0; x < KVS; ++x) {
             mbar_init(smem_addr(&k_full[x]), 1);
             mbar_init(smem_addr(&v_full[x]), 1);
-            mbar_init(smem_addr(&k_free[x]), 1);
-            mbar_init(smem_addr(&v_free[x]), 1);
+            mbar_init(smem_addr(&k_free[x]), 2);
+            mbar_init(smem_addr(&v_free[x]), 2);
         }
         s_failed = 0;
         fence_mbar_init();
@@ -455,12 +457,16 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             }
         }
         __syncwarp();
-    } else if (warp == CTRL) {
-        // ---------------------------------------------------------- MMA warp
-        // The even CTA's warp issues every product; it runs its loop as a
-        // whole warp (see umma_f16_warp).  A 16-element step of Q or K is 32
-        // bytes into the 128-byte atom row, of V (MN-major) 16 key rows.
-        if (rank == 0 && n_kt > 0) {
+    } else if (warp == CTRL || warp == CTRL + 1) {
+        // --------------------------------------------------------- MMA warps
+        // The even CTA's warps issue every product, a warp for each query
+        // tile: a product's issue lasts nearly as long as the product (the
+        // tensor core queues one or two), so what one warp spends on waits
+        // is filled by the other's products.  They run their loops as whole
+        // warps (see umma_f16_warp).
+        const int x = warp - CTRL;
+        const int32_t mine = nt[x], other = nt[1 - x];
+        if (rank == 0 && mine > 0) {
             bool failed = false;
             auto wait1 = [&](uint32_t bar, uint32_t parity) {
                 if (!failed && __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity))) {
@@ -468,70 +474,57 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     fail();
                 }
             };
-            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+            // This tile's last use of a slot of the ring; the other tile's
+            // too, if that has ended.
+            auto release = [&](unsigned long long* bar, int32_t t) {
+                umma_commit_warp<CG>(smem_addr(bar));
+                if (t >= other)
+                    umma_commit_warp<CG>(smem_addr(bar));
+            };
+            // A 16-element step of Q or K is 32 bytes into the 128-byte atom
+            // row, of V (MN-major) 16 key rows.
+            const uint64_t dq = smem_desc_sw128(sQ + x * QT_BYTES, 16, 1024);
             const uint64_t dk = smem_desc_sw128(sK, 16, 1024), dv = smem_desc_sw128(sV, 16, 1024);
-            auto issue_s = [&](int x, uint32_t at) {
-                const uint64_t a = dq + x * (QT_BYTES >> 4), b = dk + at * (KV_BYTES >> 4);
+            const uint32_t tp = tmem + P_COL + static_cast<uint32_t>(x * (BN / 2));
+            const uint32_t to = tmem + O_COL + static_cast<uint32_t>(x * D);
+            // S of tile t.  The product before it into the same columns has
+            // been read by its softmax warps when the wait on bar_ld is over.
+            auto next_s = [&](int32_t t) {
+                wait1(smem_addr(&k_full[slot(t)]), phase(t));
+                const int32_t before = x == 0 ? t - 1 : t;   // the other tile's
+                if (before >= 0 && before < other)
+                    wait1(smem_addr(&bar_ld[1 - x]), static_cast<uint32_t>(before & 1));
+                else if (t > 0)
+                    wait1(smem_addr(&bar_ld[x]), static_cast<uint32_t>((t - 1) & 1));
+                if (failed)
+                    return;
+                tc_fence_after();
+                const uint64_t b = dk + slot(t) * (KV_BYTES >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
-                    umma_f16_warp<CG>(tmem + static_cast<uint32_t>(x * BN),
-                                      a + ((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16,
+                    umma_f16_warp<CG>(tmem, dq + ((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16,
                                       b + ((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16, IDESC_S,
                                       ks > 0 ? 1u : 0u);
-            };
-            // P_X (16-bit) lies over S_X: each softmax warp's CW keys in the
-            // first CW / 2 columns of its own part.  Part c of P is the c-th
-            // 32 keys of every warp.
-            auto issue_pv = [&](int x, uint32_t at, int c, bool begin) {
-                const uint64_t b = dv + at * (KV_BYTES >> 4);
-#pragma unroll
-                for (int ks = 0; ks < BN / 16; ++ks)
-                    if ((ks * 16 % CW) / 32 == c)
-                        umma_f16_ta_warp<CG>(
-                            tmem + static_cast<uint32_t>(2 * BN + x * D),
-                            tmem + static_cast<uint32_t>(x * BN + ks * 8 + (ks * 16 / CW) * (CW / 2)),
-                            b + ks * (2048 / 16), IDESC_PV, begin && ks == 0 ? 0u : 1u);
+                umma_commit_warp<CG>(smem_addr(&bar_s[x]));
+                release(&k_free[slot(t)], t);
             };
             wait1(smem_addr(&q_full), 0u);
-            wait1(smem_addr(&k_full[0]), 0u);
-            if (!failed) {
-                tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (nt[x] > 0) {
-                        issue_s(x, 0);
-                        umma_commit_warp<CG>(smem_addr(&bar_s[x]));
-                    }
-                umma_commit_warp<CG>(smem_addr(&k_free[0]));       // S(0) done
-            }
-            for (int32_t t = 0; t < n_kt && !failed; ++t) {
+            next_s(0);
+            for (int32_t t = 0; t < mine && !failed; ++t) {
+                if (t + 1 < mine)
+                    next_s(t + 1);
                 wait1(smem_addr(&v_full[slot(t)]), phase(t));
-                if (t + 1 < n_kt)
-                    wait1(smem_addr(&k_full[slot(t + 1)]), phase(t + 1));
+                wait1(smem_addr(&bar_p[x]), static_cast<uint32_t>(t & 1));
+                if (failed)
+                    break;
+                tc_fence_after();
+                const uint64_t b = dv + slot(t) * (KV_BYTES >> 4);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (failed || t >= nt[x])
-                        continue;
-#pragma unroll
-                    for (int c = 0; c < NCH; ++c) {
-                        wait1(smem_addr(&bar_p[x][c]), static_cast<uint32_t>(t & 1));
-                        if (!failed) {
-                            tc_fence_after();
-                            issue_pv(x, slot(t), c, t == 0);
-                        }
-                    }
-                    if (failed)
-                        continue;
-                    if (x == 1 || t >= nt[1])                      // the last one of V(t)
-                        umma_commit_warp<CG>(smem_addr(&v_free[slot(t)]));
-                    const bool more = t + 1 < nt[x];
-                    if (more) {
-                        issue_s(x, slot(t + 1));
-                        if (x == 1 || t + 1 >= nt[1])              // the last one of K(t + 1)
-                            umma_commit_warp<CG>(smem_addr(&k_free[slot(t + 1)]));
-                    }
-                    umma_commit_warp<CG>(smem_addr(more ? &bar_s[x] : &bar_fin[x]));
-                }
+                for (int ks = 0; ks < BN / 16; ++ks)
+                    umma_f16_ta_warp<CG>(to, tp + ks * 8, b + ks * (2048 / 16), IDESC_PV,
+                                         t == 0 && ks == 0 ? 0u : 1u);
+                umma_commit_warp<CG>(smem_addr(&bar_pv[x]));
+                release(&v_free[slot(t)], t);
             }
         }
         __syncwarp();
@@ -550,29 +543,42 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         const int32_t limit = CAUSAL ? min(u.n_k, token + off + 1) : u.n_k;
         const int32_t limit_all = CAUSAL ? min(u.n_k, first + off + 1) : u.n_k;
         const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t s_col = static_cast<uint32_t>(x * BN + h * CW);
-        const uint32_t o_col = static_cast<uint32_t>(2 * BN + x * D + h * OW);
-        const int pair_bar = 1 + x * 4 + (warp & 3);         // the HS warps of 32 rows
+        const uint32_t s_col = static_cast<uint32_t>(h * CW);
+        const uint32_t p_col = P_COL + static_cast<uint32_t>((x * BN + h * CW) / 2);
+        const uint32_t o_col = O_COL + static_cast<uint32_t>(x * D + h * OW);
+        const int pair_bar = 5 + x * 4 + (warp & 3);         // the HS warps of 32 rows
         const int32_t my_kt = nt[x];
         float m = kNegInf, l = 0.0f;                         // l: this warp's part of the sum
         bool failed = false;                                 // warp-uniform
-        uint32_t bar_parts[NCH];
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-            bar_parts[c] = leader_addr<CG>(smem_addr(&bar_p[x][c]));
-        for (int32_t t = 0; t < my_kt; ++t) {
-            const bool ok = failed || mbar_wait_bounded(smem_addr(&bar_s[x]),
-                                                        static_cast<uint32_t>(t & 1));
-            if (__any_sync(0xffffffffu, !ok) && !failed) {
+        const uint32_t bar_loaded = leader_addr<CG>(smem_addr(&bar_ld[x]));
+        const uint32_t bar_weights = leader_addr<CG>(smem_addr(&bar_p[x]));
+        // With eight warps to a tile one of them waits on the barriers in
+        // shared memory and the others behind it at a named barrier: sixteen
+        // polling warps slow the exponentials down (d = 128, 16384 tokens:
+        // 1677 -> 1744 TFLOP/s).  With four each waits itself (d = 64: 860
+        // against 800).
+        const bool poller = HS == 1 || warp % (4 * HS) == 0;
+        auto await = [&](int id, uint32_t bar, uint32_t parity, bool wait) {
+            if (wait && poller && !failed &&
+                __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity))) {
                 failed = true;
                 fail();
             }
+            if constexpr (HS > 1)
+                named_barrier(id, 128 * HS);
             tc_fence_after();
+        };
+        for (int32_t t = 0; t < my_kt; ++t) {
+            await(1 + x, smem_addr(&bar_s[x]), static_cast<uint32_t>(t & 1), true);
             float sv[NCH][32];
 #pragma unroll
             for (int c = 0; c < NCH; ++c)
                 tmem_ld32(t_row + s_col + c * 32, sv[c]);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_leader<CG>(bar_loaded);          // S may be overwritten
             if ((t + 1) * BN > limit_all) {                  // some row has a masked key
                 const int32_t keep = limit - t * BN - h * CW;
 #pragma unroll
@@ -588,13 +594,15 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     mx = max3(mx, sv[c][j], sv[c][j + 1]);
+            // The row's maximum over its HS warps (slots by tile parity); and
+            // P V of the tile before has read P and written O.
+            if constexpr (HS > 1)
+                xmax[t & 1][x][h][r] = mx;
+            await(3 + x, smem_addr(&bar_pv[x]), static_cast<uint32_t>((t - 1) & 1), t > 0);
             if constexpr (HS > 1) {
-                const int par = t & 1;
-                xmax[par][x][h][r] = mx;
-                named_barrier(pair_bar, 32 * HS);
 #pragma unroll
                 for (int o = 0; o < HS; ++o)
-                    mx = fmaxf(mx, xmax[par][x][o][r]);
+                    mx = fmaxf(mx, xmax[t & 1][x][o][r]);
             }
             // Lazy rescaling: the reference m (base 2) moves only when the
             // tile's max exceeds it by more than 2^8; O / l and the logsumexp
@@ -624,23 +632,17 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     add2(sum0, sum1, sum0, sum1, p0, p1);
                     w[j] = Elem<T>::pack2(p0, p1);
                 }
-                tmem_st16(t_row + s_col + c * 16, w);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_leader<CG>(bar_parts[c]);    // release: O rescaled, this part of P
+                tmem_st16(t_row + p_col + c * 16, w);
             }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_leader<CG>(bar_weights);         // release: P written, O rescaled
             l = l * alpha + (sum0 + sum1);
         }
-        if (my_kt > 0) {
-            const bool ok = failed || mbar_wait_bounded(smem_addr(&bar_fin[x]), 0u);
-            if (__any_sync(0xffffffffu, !ok) && !failed) {
-                failed = true;
-                fail();
-            }
-            tc_fence_after();
-        }
+        if (my_kt > 0)
+            await(1 + x, smem_addr(&bar_pv[x]), static_cast<uint32_t>((my_kt - 1) & 1), true);
         if constexpr (HS > 1) {
             xsum[x][h][r] = l;
             named_barrier(pair_bar, 32 * HS);
@@ -649,7 +651,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             for (int o = 0; o < HS; ++o)
                 l += xsum[x][o][r];
         }
-        if (!failed && my_kt >= 0) {
+        if (!__any_sync(0xffffffffu, failed_elsewhere()) && my_kt >= 0) {
             const float inv = 1.0f / l;
             unsigned short* const dst = static_cast<unsigned short*>(p.o.data) +
                                         (u.q0 + static_cast<int64_t>(token)) * p.o.row +
@@ -738,7 +740,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == CTRL && failed_elsewhere()) {
+    if ((warp == CTRL || warp == CTRL + 1) && failed_elsewhere()) {
         if (lane == 0)
             atomicOr(&g_error_attention_packed, kErrMbarrierTimeout);
         if (rank == 0) {
@@ -746,8 +748,8 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             // this warp has issued has completed; wait for it (bounded)
             // before tensor memory is freed.
             tc_fence_after();
-            umma_commit_warp<CG>(smem_addr(&bar_drain));
-            mbar_wait_bounded(smem_addr(&bar_drain), 0u);
+            umma_commit_warp<CG>(smem_addr(&bar_drain[warp - CTRL]));
+            mbar_wait_bounded(smem_addr(&bar_drain[warp - CTRL]), 0u);
         }
         __syncwarp();
     }
