@@ -147,13 +147,14 @@ constexpr float kLazyRescaleLog2 = 8.0f;           // p <= 2^8 between rescales
 constexpr float kInf = __builtin_inff();
 
 // CTAs that share each product, keys per tile, warps that share a row of S,
-// ring slots of K and of V, CTAs per SM.
+// ring slots of K and of V, CTAs per SM, output columns that a warp stages at
+// a time.
 template <int D> struct Shape;
 template <> struct Shape<128> {
-    static constexpr int CG = 2, BN = 128, HS = 2, KVS = 4, CTAS = 1;
+    static constexpr int CG = 2, BN = 128, HS = 2, KVS = 3, CTAS = 1, EC = 32;
 };
 template <> struct Shape<64> {
-    static constexpr int CG = 1, BN = 64, HS = 1, KVS = 4, CTAS = 2;
+    static constexpr int CG = 1, BN = 128, HS = 2, KVS = 4, CTAS = 1, EC = 32;
 };
 
 template <int D>
@@ -166,7 +167,7 @@ template <int D>
 constexpr int packed_smem()
 {
     using S = Shape<D>;
-    return (2 * kBM * D + 2 * S::KVS * (S::BN / S::CG) * D) * 2 + 1024;
+    return (2 * kBM * D + 2 * S::KVS * (S::BN / S::CG) * D) * 2 + 8 * S::HS * 32 * S::EC * 2 + 1024;
 }
 
 // The unit of work of a CTA (pair): `tokens` query tokens of one sequence,
@@ -199,95 +200,144 @@ __device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int32_t 
     return units - first;
 }
 
-// Unit number `rank` in the order in which units are handed out, by a warp:
-// the units that visit most key tiles first, so that the ones dispatched last
-// are short (above kRanked sequences: the order of the sequences).
+// Finds unit number `rank` in the order in which units are handed out, by a
+// warp: the units that visit most key tiles first, so that the ones dispatched
+// last are short.  The sequences' bounds are read once and kept, four to a
+// lane; above kRanked sequences the order is that of the sequences instead,
+// and the walk goes on from where the last one ended.
 constexpr int kRanked = 128;
 
-__device__ Unit find_unit(const PackedProblem& p, int64_t rank, int32_t tokens, int bn, bool report)
-{
-    const int lane = threadIdx.x & 31;
-    Unit u = {};
-    auto lengths = [&](int64_t s, int32_t& q0, int32_t& n_q, int32_t& k0, int32_t& n_k) {
+struct UnitFinder {
+    int32_t q0[4], n_q[4], k0[4], n_k[4];
+    int32_t most;                                  // most key tiles of a unit
+    int64_t total;                                 // units (ranked), or past the end
+    int64_t at, before;                            // unranked: sequence block, units before it
+
+    __device__ __forceinline__ void lengths(const PackedProblem& p, int64_t s, int i, bool report)
+    {
         int64_t a = 0, b = 0, c = 0, d = 0;
         if (s < p.n_seqs && !sequence_of(p, s, a, b, c, d) && report)
             atomicOr(&g_error_attention_packed, kErrBadIndex);
-        q0 = static_cast<int32_t>(a);
-        n_q = static_cast<int32_t>(b);
-        k0 = static_cast<int32_t>(c);
-        n_k = static_cast<int32_t>(d);
-    };
-    auto sum = [](int64_t v) {
+        q0[i] = static_cast<int32_t>(a);
+        n_q[i] = static_cast<int32_t>(b);
+        k0[i] = static_cast<int32_t>(c);
+        n_k[i] = static_cast<int32_t>(d);
+    }
+
+    // Units that visit at least x key tiles.
+    __device__ __forceinline__ int32_t count(const PackedProblem& p, int32_t tokens, int bn,
+                                             int32_t x) const
+    {
+        int32_t n = 0, first;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    };
-    int32_t q0, n_q, k0, n_k, first;
-    const bool ranked = p.n_seqs <= kRanked;
-    int32_t level = 0;                             // key tiles of the unit sought
-    int64_t above = 0;                             // units of higher levels
-    if (ranked) {
-        int32_t most = 0;
-        for (int64_t s = lane; s < p.n_seqs; s += 32) {
-            lengths(s, q0, n_q, k0, n_k);
-            most = n_q > 0 ? max(most, (n_k + bn - 1) / bn) : most;
+        for (int i = 0; i < 4; ++i)
+            n += units_with(n_q[i], n_k[i], tokens, bn, p.causal, x, first);
+        return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+    }
+
+    __device__ void init(const PackedProblem& p, int32_t tokens, int bn, bool report)
+    {
+        const int lane = threadIdx.x & 31;
+        at = before = 0;
+        total = INT64_MAX;
+        if (p.n_seqs > kRanked) {
+            for (int64_t s = lane; report && s < p.n_seqs; s += 32)
+                lengths(p, s, 0, true);
+            return;
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        int32_t lo = 0, hi = most + 1;             // N(lo) > rank >= N(hi)
-        for (int pass = 0; lo + 1 < hi || pass == 0; ++pass) {
-            // The first pass asks for level 0: all units.
-            const int32_t x = pass == 0 ? 0 : lo + (hi - lo) / 2;
-            int64_t n = 0;
-            for (int64_t s = lane; s < p.n_seqs; s += 32) {
-                lengths(s, q0, n_q, k0, n_k);
-                n += units_with(n_q, n_k, tokens, bn, p.causal, x, first);
+        int32_t longest = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lengths(p, i * 32 + lane, i, report);
+            longest = n_q[i] > 0 ? max(longest, (n_k[i] + bn - 1) / bn) : longest;
+        }
+        most = __reduce_max_sync(0xffffffffu, longest);
+        total = count(p, tokens, bn, 0);
+    }
+
+    // The first of the 32 sequences in slot i whose units, n to a lane, hold
+    // unit number `left`; subtracts the units passed from `left`.
+    __device__ __forceinline__ int pick(int32_t n, int64_t& left, int64_t& passed)
+    {
+        const int lane = threadIdx.x & 31;
+        int32_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += up;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > left);
+        passed = __shfl_sync(0xffffffffu, upto, 31);
+        if (!past) {
+            left -= passed;
+            return -1;
+        }
+        const int lane_of = __ffs(past) - 1;
+        left -= __shfl_sync(0xffffffffu, upto - n, lane_of);
+        return lane_of;
+    }
+
+    __device__ __forceinline__ Unit unit(int i, int lane_of, int32_t tile) const
+    {
+        Unit u;
+        u.q0 = __shfl_sync(0xffffffffu, q0[i], lane_of);
+        u.n_q = __shfl_sync(0xffffffffu, n_q[i], lane_of);
+        u.k0 = __shfl_sync(0xffffffffu, k0[i], lane_of);
+        u.n_k = __shfl_sync(0xffffffffu, n_k[i], lane_of);
+        u.tile = tile;
+        u.head = 0;
+        u.ok = 1;
+        return u;
+    }
+
+    __device__ Unit find(const PackedProblem& p, int64_t rank, int32_t tokens, int bn)
+    {
+        const int lane = threadIdx.x & 31;
+        Unit none = {};
+        if (rank >= total)
+            return none;
+        int64_t passed;
+        if (p.n_seqs > kRanked) {
+            if (rank < before)
+                at = before = 0;
+            for (; at < p.n_seqs; at += 32) {
+                lengths(p, at + lane, 0, false);
+                int64_t left = rank - before;
+                const int32_t n = (n_q[0] + tokens - 1) / tokens;
+                const int l = pick(n, left, passed);
+                if (l >= 0)                        // longest first within the sequence
+                    return unit(0, l, __shfl_sync(0xffffffffu, n, l) - 1 -
+                                          static_cast<int32_t>(left));
+                before += passed;
             }
-            n = sum(n);
-            if (pass == 0) {
-                if (n <= rank)
-                    return u;
-            } else if (n > rank) {
+            total = rank;
+            at = before = 0;
+            return none;
+        }
+        int32_t lo = 0, hi = most + 1, above = 0;  // count(lo) > rank >= count(hi) = above
+        while (lo + 1 < hi) {
+            const int32_t x = lo + (hi - lo) / 2, n = count(p, tokens, bn, x);
+            if (n > rank) {
                 lo = x;
             } else {
                 hi = x;
                 above = n;
             }
         }
-        level = lo;
-    }
-    int64_t left = rank - above;
-    for (int64_t s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        lengths(s0 + lane, q0, n_q, k0, n_k);
-        int32_t next, n = units_with(n_q, n_k, tokens, bn, p.causal, ranked ? level : 0, first);
-        const int32_t end = first + n;
-        if (ranked)
-            n -= units_with(n_q, n_k, tokens, bn, p.causal, level + 1, next);
-        int64_t upto = n;
+        int64_t left = rank - above;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o)
-                upto += up;
+        for (int i = 0; i < 4; ++i) {
+            int32_t first, next;
+            int32_t n = units_with(n_q[i], n_k[i], tokens, bn, p.causal, lo, first);
+            n -= units_with(n_q[i], n_k[i], tokens, bn, p.causal, lo + 1, next);
+            const int l = pick(n, left, passed);
+            if (l >= 0)
+                return unit(i, l, __shfl_sync(0xffffffffu, first, l) + static_cast<int32_t>(left));
         }
-        const unsigned past = __ballot_sync(0xffffffffu, upto > left);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            // Longest first within the sequence when units are not ranked.
-            const int32_t i = static_cast<int32_t>(left - (upto - n));
-            const int32_t tile = ranked ? first + i : end - 1 - i;
-            u.q0 = __shfl_sync(0xffffffffu, q0, at);
-            u.n_q = __shfl_sync(0xffffffffu, n_q, at);
-            u.k0 = __shfl_sync(0xffffffffu, k0, at);
-            u.n_k = __shfl_sync(0xffffffffu, n_k, at);
-            u.tile = __shfl_sync(0xffffffffu, tile, at);
-            u.ok = 1;
-            return u;
-        }
-        left -= __shfl_sync(0xffffffffu, upto, 31);
+        return none;
     }
-    return u;
-}
+};
 
 template <typename T, int D, bool CAUSAL>
 __global__ void __launch_bounds__(packed_threads<D>(), Shape<D>::CTAS)
@@ -297,7 +347,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2)
 {
     using S = Shape<D>;
-    constexpr int CG = S::CG, BN = S::BN, HS = S::HS, KVS = S::KVS;
+    constexpr int CG = S::CG, BN = S::BN, HS = S::HS, KVS = S::KVS, EC = S::EC;
     constexpr bool kBF16 = Elem<T>::kNegInfBits == 0xff80u;
     constexpr uint32_t QT_BYTES = kBM * D * 2;               // a query tile
     constexpr uint32_t KV_BYTES = BN / CG * D * 2;           // this CTA's part of a key tile
@@ -308,26 +358,34 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     constexpr uint32_t IDESC_PV = umma_idesc(kBM * CG, D, kBF16, true);
     // Tensor memory: S of either query tile (BN columns), P of each (BN / 2),
     // O of each (D).
-    constexpr uint32_t P_COL = BN, O_COL = 2 * BN, TMEM_COLS = 2 * BN + 2 * D;
-    static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "a power of two");
+    constexpr uint32_t P_COL = BN, O_COL = 2 * BN, TMEM_COLS = 2 * BN + 2 * D <= 256 ? 256 : 512;
+    static_assert(2 * BN + 2 * D <= 512, "all of tensor memory");
     constexpr int CW = BN / HS;                              // keys of S per softmax warp
     constexpr int NCH = CW / 32;                             // 32-column chunks per warp
     constexpr int OW = D / HS;                               // O columns per softmax warp
-    constexpr int CTRL = 2 * 4 * HS, LOADW = CTRL + 2;       // MMA warps, copy warp
+    constexpr int SOFT = 2 * 4 * HS;                         // softmax warps
+    constexpr int CTRL = SOFT, LOADW = CTRL + 2;             // MMA warps, copy warp
     extern __shared__ __align__(128) unsigned char pk_smem[];
-    __shared__ __align__(8) unsigned long long bar_s[2], bar_ld[2], bar_p[2], bar_pv[2], bar_drain[2];
-    __shared__ __align__(8) unsigned long long q_full, k_full[KVS], v_full[KVS];
+    __shared__ __align__(8) unsigned long long bar_s[2], bar_ld[2], bar_p[2], bar_pv[2];
+    __shared__ __align__(8) unsigned long long o_free[2], bar_end, bar_drain[2];
+    __shared__ __align__(8) unsigned long long q_full, q_free, k_full[KVS], v_full[KVS];
     __shared__ __align__(8) unsigned long long k_free[KVS], v_free[KVS];
+    __shared__ __align__(8) unsigned long long unit_full[2], unit_free[2];
+    __shared__ __align__(8) unsigned long long next_full[2], next_free[2];
+    __shared__ __align__(16) uint4 s_next[2];                // answers of cluster launch control
+    __shared__ Unit s_unit[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int s_failed;
-    __shared__ Unit s_unit;
-    // Row maxima (by tile parity) and final sums of the warps sharing a row.
+    __shared__ int s_stop[2][2][4];
+    // Row maxima (by tile parity) and final sums of the warps sharing a row,
+    // and their rows to be done again.
     __shared__ float xmax[HS > 1 ? 2 : 1][2][HS][kBM];
     __shared__ float xsum[2][HS][kBM];
     __shared__ unsigned xredo[2][HS][4];
 
     const uint32_t base = (smem_addr(pk_smem) + 1023u) & ~1023u;   // swizzle atoms
     const uint32_t sQ = base, sK = sQ + 2 * QT_BYTES, sV = sK + KVS * KV_BYTES;
+    const uint32_t sO = sV + KVS * KV_BYTES;                 // 32 rows x EC columns per softmax warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank<CG>();
     const int gp = 1 << gp_log2;
@@ -342,9 +400,16 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             mbar_init(smem_addr(&bar_p[x]), 4 * HS * CG);
             mbar_init(smem_addr(&bar_ld[x]), 4 * HS * CG);
             mbar_init(smem_addr(&bar_pv[x]), 1);
+            mbar_init(smem_addr(&o_free[x]), 4 * HS * CG);
             mbar_init(smem_addr(&bar_drain[x]), 1);
+            mbar_init(smem_addr(&unit_full[x]), 1);
+            mbar_init(smem_addr(&unit_free[x]), SOFT + (rank == 0 ? 2 : 0));
+            mbar_init(smem_addr(&next_full[x]), 1);
+            mbar_init(smem_addr(&next_free[x]), CG);
         }
+        mbar_init(smem_addr(&bar_end), 2 * 4 * HS * CG + 2);
         mbar_init(smem_addr(&q_full), 1);
+        mbar_init(smem_addr(&q_free), 2);
         for (int x = 0; x < KVS; ++x) {
             mbar_init(smem_addr(&k_full[x]), 1);
             mbar_init(smem_addr(&v_full[x]), 1);
@@ -354,109 +419,151 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         s_failed = 0;
         fence_mbar_init();
     }
-    pdl_launch_dependents();
-    pdl_wait();
-    if (warp == LOADW) {
-        const int64_t blocks = p.n_heads >> gp_log2;
-        const int64_t unit = blockIdx.x / CG;
-        Unit u = find_unit(p, unit / blocks, tokens, BN, unit == 0 && rank == 0);
-        u.head = static_cast<int32_t>(unit % blocks) << gp_log2;
-        if (lane == 0)
-            s_unit = u;
-    }
     tc_fence_before();
     group_sync<CG>();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const Unit u = s_unit;
-    const int kvh = u.head / (p.n_heads / p.n_kv_heads);
-    const int32_t off = u.n_k - u.n_q;
-    // Key tiles that query tile x visits (both CTAs' parts of it), -1 when it
-    // has no tokens at all.
-    auto tiles_of = [&](int x) -> int32_t {
+    pdl_launch_dependents();
+    pdl_wait();
+
+    auto fail = [&] { *reinterpret_cast<volatile int*>(&s_failed) = 1; };
+    auto failed_elsewhere = [&] {
+        return __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_failed) != 0) != 0;
+    };
+    // Every wait: by a whole warp in uniform control flow, bounded; after one
+    // that ran out the warp waits for nothing more.
+    bool failed = false;
+    auto wait1 = [&](unsigned long long* bar, uint32_t parity) {
+        if (!failed && __any_sync(0xffffffffu, !mbar_wait_bounded(smem_addr(bar), parity & 1u))) {
+            failed = true;
+            fail();
+        }
+    };
+    // Key tiles that query tile x of a unit visits (both CTAs' parts of it),
+    // -1 when it has no tokens at all.
+    auto tiles_of = [&](const Unit& u, int x) -> int32_t {
         const int32_t begin = u.tile * tokens + x * CG * tile_tokens;
-        if (!u.ok || begin >= u.n_q)
+        if (u.ok <= 0 || begin >= u.n_q)
             return -1;
         int32_t lim = u.n_k;
-        if (CAUSAL) {
-            const int32_t end = min(begin + CG * tile_tokens, u.n_q);
-            lim = min(lim, end + off);
-        }
+        if (CAUSAL)
+            lim = min(lim, min(begin + CG * tile_tokens, u.n_q) + u.n_k - u.n_q);
         return lim <= 0 ? 0 : (lim + BN - 1) / BN;
     };
-    const int32_t nt[2] = {tiles_of(0), tiles_of(1)};
-    const int32_t n_kt = max(max(nt[0], nt[1]), 0);
+    // Tile number t, counted through all units, lies in ring slot t % KVS.
+    auto slot = [](uint32_t t) { return t % KVS; };
+    auto phase = [](uint32_t t) { return (t / KVS) & 1u; };
+    const int group = p.n_heads / p.n_kv_heads;
 
-    auto slot = [](int32_t t) { return static_cast<uint32_t>(t) % KVS; };
-    auto phase = [](int32_t t) { return (static_cast<uint32_t>(t) / KVS) & 1u; };
-    auto fail = [&] { *reinterpret_cast<volatile int*>(&s_failed) = 1; };
-    auto failed_elsewhere = [&] { return *reinterpret_cast<volatile int*>(&s_failed) != 0; };
     if (warp == LOADW) {
         // --------------------------------------------------------- copy warp
-        // Each CTA copies its own query tiles, its rows of K and its columns
-        // of V; all complete on the even CTA's barriers, whose copy lane
-        // announces the bytes of both.
-        if (lane == 0 && n_kt > 0) {
-            bool failed = false;
-            auto wait1 = [&](uint32_t bar, uint32_t parity) {
-                if (!failed && !mbar_wait_bounded(bar, parity)) {
-                    failed = true;
-                    fail();
+        // Hands out the units (its own cluster's, then those of clusters not
+        // yet launched, which it takes over one at a time) and copies their
+        // operands.  Each CTA copies its own query tiles, its rows of K and
+        // its columns of V; all complete on the even CTA's barriers, where
+        // the bytes of both are announced.
+        const bool one = lane == 0;
+        const int64_t blocks = p.n_heads >> gp_log2;
+        UnitFinder finder;
+        finder.init(p, tokens, BN, blockIdx.x == 0);
+        int64_t index = blockIdx.x / CG;
+        uint32_t kv = 0, q_uses = 0;
+        auto announce = [&](unsigned long long* bar, uint32_t bytes) {
+            if (one && rank == 0)
+                mbar_arrive_expect_tx(smem_addr(bar), bytes * CG);
+            return leader_addr<CG>(smem_addr(bar));
+        };
+        for (uint32_t i = 0; index >= 0 && !failed; ++i) {
+            // Ask for the next unit: the answer of two units ago has been
+            // read by both CTAs.
+            if (one)
+                mbar_arrive_expect_tx(smem_addr(&next_full[i & 1]), 16);
+            if (rank == 0) {
+                if (i >= 2)
+                    wait1(&next_free[i & 1], (i - 2) >> 1);
+                if (one)
+                    clc_try_cancel<CG>(smem_addr(&s_next[i & 1]), smem_addr(&next_full[i & 1]));
+            }
+            Unit u = finder.find(p, index / blocks, tokens, BN);
+            u.head = static_cast<int32_t>(index % blocks) << gp_log2;
+            if (i >= 2)
+                wait1(&unit_free[i & 1], (i - 2) >> 1);
+            if (one) {
+                s_unit[i & 1] = u;
+                mbar_arrive(smem_addr(&unit_full[i & 1]));
+            }
+            const int32_t n_kt = max(tiles_of(u, 0), tiles_of(u, 1));
+            if (n_kt > 0) {
+                const int kvh = u.head / group;
+                if (q_uses > 0)
+                    wait1(&q_free, q_uses - 1);
+                ++q_uses;
+                const uint32_t bar_q = announce(&q_full, 2 * QT_BYTES);
+                if (one && !failed) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d<CG>(sQ + x * QT_BYTES + c * (kBM * 128), &map_q, c * 64,
+                                            u.head, u.q0 + u.tile * tokens +
+                                            (x * CG + static_cast<int>(rank)) * tile_tokens, bar_q);
                 }
-            };
-            auto announce = [&](unsigned long long* bar, uint32_t bytes) {
-                if (rank == 0)
-                    mbar_arrive_expect_tx(smem_addr(bar), bytes * CG);
-                return leader_addr<CG>(smem_addr(bar));
-            };
-            int32_t k_issued = 0, v_issued = 0;
-            auto load_k = [&](int32_t t) {
-                const uint32_t bar = announce(&k_full[slot(t)], KV_BYTES);
+                for (int32_t t = 0; t < n_kt && !failed; ++t, ++kv) {
+                    if (kv >= KVS)
+                        wait1(&k_free[slot(kv)], (kv - KVS) / KVS);          // every S done
+                    const uint32_t bar_k = announce(&k_full[slot(kv)], KV_BYTES);
+                    if (one && !failed) {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d<CG>(sK + slot(t) * KV_BYTES + c * (KR * 128), &map_k, c * 64, kvh,
-                                    u.k0 + t * BN + static_cast<int>(rank) * KR, bar);
-                k_issued = t + 1;
-            };
-            auto load_v = [&](int32_t t) {
-                const uint32_t bar = announce(&v_full[slot(t)], KV_BYTES);
-                tma_load_3d<CG>(sV + slot(t) * KV_BYTES, &map_v, static_cast<int>(rank) * VD, kvh,
-                                u.k0 + t * BN, bar);
-                v_issued = t + 1;
-            };
-            const uint32_t bar_q = announce(&q_full, 2 * QT_BYTES);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d<CG>(sQ + x * QT_BYTES + c * (kBM * 128), &map_q, c * 64, u.head,
-                                    u.q0 + u.tile * tokens +
-                                        (x * CG + static_cast<int>(rank)) * tile_tokens, bar_q);
-            for (int32_t t = 0; t < KVS && t < n_kt; ++t) {
-                load_k(t);
-                load_v(t);
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d<CG>(sK + slot(kv) * KV_BYTES + c * (KR * 128), &map_k,
+                                            c * 64, kvh, u.k0 + t * BN +
+                                            static_cast<int>(rank) * KR, bar_k);
+                    }
+                    if (kv >= KVS)
+                        wait1(&v_free[slot(kv)], (kv - KVS) / KVS);          // every P V done
+                    const uint32_t bar_v = announce(&v_full[slot(kv)], KV_BYTES);
+                    if (one && !failed)
+                        tma_load_3d<CG>(sV + slot(kv) * KV_BYTES, &map_v,
+                                        static_cast<int>(rank) * VD, kvh, u.k0 + t * BN, bar_v);
+                    if (failed_elsewhere())
+                        failed = true;
+                }
             }
-            for (int32_t t = 0; t + KVS < n_kt && !failed; ++t) {
-                wait1(smem_addr(&k_free[slot(t)]), phase(t));      // every S(t) done
-                if (failed || failed_elsewhere())
-                    break;
-                load_k(t + KVS);
-                wait1(smem_addr(&v_free[slot(t)]), phase(t));      // every P V(t) done
-                if (failed || failed_elsewhere())
-                    break;
-                load_v(t + KVS);
-            }
-            if (rank == 0 && (failed || failed_elsewhere())) {
-                // Let the copies still in flight land (bounded; after one
-                // wait that ran out the others are not waited for).
-                bool ok = mbar_wait_bounded(smem_addr(&q_full), 0u);
-                for (int32_t t = k_issued > KVS ? k_issued - KVS : 0; t < k_issued && ok; ++t)
-                    ok = mbar_wait_bounded(smem_addr(&k_full[slot(t)]), phase(t));
-                for (int32_t t = v_issued > KVS ? v_issued - KVS : 0; t < v_issued && ok; ++t)
-                    ok = mbar_wait_bounded(smem_addr(&v_full[slot(t)]), phase(t));
+            // The answer; both CTAs get the same.
+            const bool answered =
+                __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&next_full[i & 1]), (i >> 1) & 1u));
+            int64_t next = -1;
+            if (answered)
+                next = clc_first_cta(smem_addr(&s_next[i & 1]));
+            else
+                fail();
+            fence_proxy_async_smem();                        // read before it is written again
+            __syncwarp();
+            if (one)
+                mbar_arrive_leader<CG>(leader_addr<CG>(smem_addr(&next_free[i & 1])));
+            index = next < 0 ? -1 : next / CG;
+            if (index < 0) {
+                // No unit is left: say so.
+                ++i;
+                if (i >= 2)
+                    wait1(&unit_free[i & 1], (i - 2) >> 1);
+                if (one) {
+                    s_unit[i & 1].ok = -1;
+                    mbar_arrive(smem_addr(&unit_full[i & 1]));
+                }
             }
         }
-        __syncwarp();
+        if (rank == 0 && failed_elsewhere()) {
+            // Let the copies still in flight land (bounded; after one wait
+            // that ran out the others are not waited for).
+            failed = false;
+            if (q_uses > 0)
+                wait1(&q_full, q_uses - 1);
+            for (uint32_t t = kv > KVS ? kv - KVS : 0; t < kv; ++t) {
+                wait1(&k_full[slot(t)], phase(t));
+                wait1(&v_full[slot(t)], phase(t));
+            }
+        }
     } else if (warp == CTRL || warp == CTRL + 1) {
         // --------------------------------------------------------- MMA warps
         // The even CTA's warps issue every product, a warp for each query
@@ -465,69 +572,96 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         // is filled by the other's products.  They run their loops as whole
         // warps (see umma_f16_warp).
         const int x = warp - CTRL;
-        const int32_t mine = nt[x], other = nt[1 - x];
-        if (rank == 0 && mine > 0) {
-            bool failed = false;
-            auto wait1 = [&](uint32_t bar, uint32_t parity) {
-                if (!failed && __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity))) {
-                    failed = true;
-                    fail();
-                }
-            };
-            // This tile's last use of a slot of the ring; the other tile's
-            // too, if that has ended.
-            auto release = [&](unsigned long long* bar, int32_t t) {
-                umma_commit_warp<CG>(smem_addr(bar));
-                if (t >= other)
-                    umma_commit_warp<CG>(smem_addr(bar));
-            };
-            // A 16-element step of Q or K is 32 bytes into the 128-byte atom
-            // row, of V (MN-major) 16 key rows.
-            const uint64_t dq = smem_desc_sw128(sQ + x * QT_BYTES, 16, 1024);
-            const uint64_t dk = smem_desc_sw128(sK, 16, 1024), dv = smem_desc_sw128(sV, 16, 1024);
-            const uint32_t tp = tmem + P_COL + static_cast<uint32_t>(x * (BN / 2));
-            const uint32_t to = tmem + O_COL + static_cast<uint32_t>(x * D);
+        // A 16-element step of Q or K is 32 bytes into the 128-byte atom row,
+        // of V (MN-major) 16 key rows.
+        const uint64_t dq = smem_desc_sw128(sQ + x * QT_BYTES, 16, 1024);
+        const uint64_t dk = smem_desc_sw128(sK, 16, 1024), dv = smem_desc_sw128(sV, 16, 1024);
+        const uint32_t tp = tmem + P_COL + static_cast<uint32_t>(x * (BN / 2));
+        const uint32_t to = tmem + O_COL + static_cast<uint32_t>(x * D);
+        // A wait is on the parity of a phase, so no warp may fall two phases
+        // behind a barrier that it waits on.  Within a unit the two tiles'
+        // products alternate; past a tile's own last key tile its warp still
+        // waits for every K and V and gives it back, and bar_end, which both
+        // warps and every softmax warp arrive at, closes the unit's S columns.
+        // Of the units before: key tiles, S products of this query tile and
+        // of the other, units with work for this tile, units with any.
+        uint32_t kv = 0, done = 0, done_other = 0, units = 0, q_uses = 0;
+        for (uint32_t i = 0; rank == 0 && !failed; ++i) {
+            wait1(&unit_full[i & 1], i >> 1);
+            if (failed)
+                break;
+            const Unit u = s_unit[i & 1];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&unit_free[i & 1]));
+            if (u.ok < 0)
+                break;
+            const int32_t mine = max(tiles_of(u, x), 0), other = max(tiles_of(u, 1 - x), 0);
             // S of tile t.  The product before it into the same columns has
             // been read by its softmax warps when the wait on bar_ld is over.
             auto next_s = [&](int32_t t) {
-                wait1(smem_addr(&k_full[slot(t)]), phase(t));
+                const uint32_t k = kv + static_cast<uint32_t>(t);
+                wait1(&k_full[slot(k)], phase(k));
                 const int32_t before = x == 0 ? t - 1 : t;   // the other tile's
                 if (before >= 0 && before < other)
-                    wait1(smem_addr(&bar_ld[1 - x]), static_cast<uint32_t>(before & 1));
+                    wait1(&bar_ld[1 - x], done_other + static_cast<uint32_t>(before));
                 else if (t > 0)
-                    wait1(smem_addr(&bar_ld[x]), static_cast<uint32_t>((t - 1) & 1));
+                    wait1(&bar_ld[x], done + static_cast<uint32_t>(t - 1));
                 if (failed)
                     return;
                 tc_fence_after();
-                const uint64_t b = dk + slot(t) * (KV_BYTES >> 4);
+                const uint64_t b = dk + slot(k) * (KV_BYTES >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     umma_f16_warp<CG>(tmem, dq + ((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16,
                                       b + ((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16, IDESC_S,
                                       ks > 0 ? 1u : 0u);
                 umma_commit_warp<CG>(smem_addr(&bar_s[x]));
-                release(&k_free[slot(t)], t);
+                umma_commit_warp<CG>(smem_addr(&k_free[slot(k)]));
+                if (t + 1 == mine)
+                    umma_commit_warp<CG>(smem_addr(&q_free));
             };
-            wait1(smem_addr(&q_full), 0u);
-            next_s(0);
+            if (i > 0)
+                wait1(&bar_end, i - 1);                      // every S of the unit before is read
+            if (mine > 0 || other > 0)
+                wait1(&q_full, q_uses++);
+            if (mine > 0)
+                next_s(0);
+            else if (other > 0)
+                umma_commit_warp<CG>(smem_addr(&q_free));
             for (int32_t t = 0; t < mine && !failed; ++t) {
                 if (t + 1 < mine)
                     next_s(t + 1);
-                wait1(smem_addr(&v_full[slot(t)]), phase(t));
-                wait1(smem_addr(&bar_p[x]), static_cast<uint32_t>(t & 1));
+                const uint32_t k = kv + static_cast<uint32_t>(t);
+                wait1(&v_full[slot(k)], phase(k));
+                if (t == 0 && units > 0)
+                    wait1(&o_free[x], units - 1);            // O of the unit before has been read
+                wait1(&bar_p[x], done + static_cast<uint32_t>(t));
                 if (failed)
                     break;
                 tc_fence_after();
-                const uint64_t b = dv + slot(t) * (KV_BYTES >> 4);
+                const uint64_t b = dv + slot(k) * (KV_BYTES >> 4);
 #pragma unroll
                 for (int ks = 0; ks < BN / 16; ++ks)
                     umma_f16_ta_warp<CG>(to, tp + ks * 8, b + ks * (2048 / 16), IDESC_PV,
                                          t == 0 && ks == 0 ? 0u : 1u);
                 umma_commit_warp<CG>(smem_addr(&bar_pv[x]));
-                release(&v_free[slot(t)], t);
+                umma_commit_warp<CG>(smem_addr(&v_free[slot(k)]));
             }
+            for (int32_t t = mine; t < other && !failed; ++t) {
+                const uint32_t k = kv + static_cast<uint32_t>(t);
+                wait1(&k_full[slot(k)], phase(k));
+                umma_commit_warp<CG>(smem_addr(&k_free[slot(k)]));
+                wait1(&v_full[slot(k)], phase(k));
+                umma_commit_warp<CG>(smem_addr(&v_free[slot(k)]));
+            }
+            if (lane == 0)
+                mbar_arrive(smem_addr(&bar_end));
+            kv += static_cast<uint32_t>(max(mine, other));
+            done += static_cast<uint32_t>(mine);
+            done_other += static_cast<uint32_t>(other);
+            units += mine > 0 ? 1u : 0u;
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------- softmax warps
         // Warp w: query tile x, TMEM lane group w % 4 (rows 32 (w % 4) ..),
@@ -535,153 +669,180 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         // share a row.
         const int x = warp / (4 * HS), h = (warp / 4) % HS;
         const int r = (warp & 3) * 32 + lane;                // row of the tile = TMEM lane
-        const int32_t first = u.tile * tokens + (x * CG + static_cast<int>(rank)) * tile_tokens;
-        const int32_t token = first + (r >> gp_log2);        // of the sequence
-        const int32_t head = u.head + (r & (gp - 1));
-        const bool real = u.ok && token < u.n_q;
-        // Keys visible to this row, and to every row of the tile.
-        const int32_t limit = CAUSAL ? min(u.n_k, token + off + 1) : u.n_k;
-        const int32_t limit_all = CAUSAL ? min(u.n_k, first + off + 1) : u.n_k;
         const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_col = static_cast<uint32_t>(h * CW);
         const uint32_t p_col = P_COL + static_cast<uint32_t>((x * BN + h * CW) / 2);
         const uint32_t o_col = O_COL + static_cast<uint32_t>(x * D + h * OW);
         const int pair_bar = 5 + x * 4 + (warp & 3);         // the HS warps of 32 rows
-        const int32_t my_kt = nt[x];
-        float m = kNegInf, l = 0.0f;                         // l: this warp's part of the sum
-        bool failed = false;                                 // warp-uniform
         const uint32_t bar_loaded = leader_addr<CG>(smem_addr(&bar_ld[x]));
         const uint32_t bar_weights = leader_addr<CG>(smem_addr(&bar_p[x]));
+        const uint32_t bar_over = leader_addr<CG>(smem_addr(&bar_end));
+        const uint32_t bar_output = leader_addr<CG>(smem_addr(&o_free[x]));
+        const uint32_t stage = sO + static_cast<uint32_t>(warp * 32 * EC * 2);
         // With eight warps to a tile one of them waits on the barriers in
         // shared memory and the others behind it at a named barrier: sixteen
         // polling warps slow the exponentials down (d = 128, 16384 tokens:
         // 1677 -> 1744 TFLOP/s).  With four each waits itself (d = 64: 860
         // against 800).
         const bool poller = HS == 1 || warp % (4 * HS) == 0;
-        auto await = [&](int id, uint32_t bar, uint32_t parity, bool wait) {
-            if (wait && poller && !failed &&
-                __any_sync(0xffffffffu, !mbar_wait_bounded(bar, parity))) {
-                failed = true;
-                fail();
-            }
+        auto await = [&](int id, unsigned long long* bar, uint32_t parity, bool wait) {
+            if (wait && poller)
+                wait1(bar, parity);
             if constexpr (HS > 1)
                 named_barrier(id, 128 * HS);
-            tc_fence_after();
         };
-        for (int32_t t = 0; t < my_kt; ++t) {
-            await(1 + x, smem_addr(&bar_s[x]), static_cast<uint32_t>(t & 1), true);
-            float sv[NCH][32];
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-                tmem_ld32(t_row + s_col + c * 32, sv[c]);
-            tmem_wait_ld();
-            tc_fence_before();
+        uint32_t done = 0;                                   // key tiles of the units before
+        for (uint32_t i = 0;; ++i) {
+            // The tile's warps stop together (they meet at named barriers): the
+            // one that waits says so, in the slot of this unit.
+            if (poller) {
+                wait1(&unit_full[i & 1], i >> 1);
+                const int stop = failed_elsewhere();
+                if (lane == 0)
+                    s_stop[i & 1][x][HS == 1 ? warp & 3 : 0] = stop;
+                __syncwarp();
+            }
+            if constexpr (HS > 1)
+                named_barrier(1 + x, 128 * HS);
+            if (s_stop[i & 1][x][HS == 1 ? warp & 3 : 0])
+                break;
+            const Unit u = s_unit[i & 1];
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_leader<CG>(bar_loaded);          // S may be overwritten
-            if ((t + 1) * BN > limit_all) {                  // some row has a masked key
-                const int32_t keep = limit - t * BN - h * CW;
+                mbar_arrive(smem_addr(&unit_free[i & 1]));
+            if (u.ok < 0)
+                break;
+            const int32_t my_kt = tiles_of(u, x);
+            if (my_kt <= 0 && lane == 0)
+                mbar_arrive_leader<CG>(bar_over);
+            if (my_kt < 0)
+                continue;
+            const int32_t off = u.n_k - u.n_q;
+            const int32_t first = u.tile * tokens + (x * CG + static_cast<int>(rank)) * tile_tokens;
+            const int32_t token = first + (r >> gp_log2);    // of the sequence
+            // Keys visible to this row, and to every row of the tile.
+            const int32_t limit = CAUSAL ? min(u.n_k, token + off + 1) : u.n_k;
+            const int32_t limit_all = CAUSAL ? min(u.n_k, first + off + 1) : u.n_k;
+            float m = kNegInf, l = 0.0f;                     // l: this warp's part of the sum
+            for (int32_t t = 0; t < my_kt; ++t) {
+                await(1 + x, &bar_s[x], done + static_cast<uint32_t>(t), true);
+                tc_fence_after();
+                float sv[NCH][32];
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                    tmem_ld32(t_row + s_col + c * 32, sv[c]);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {                             // S may be overwritten
+                    mbar_arrive_leader<CG>(bar_loaded);
+                    if (t + 1 == my_kt)
+                        mbar_arrive_leader<CG>(bar_over);
+                }
+                if ((t + 1) * BN > limit_all) {              // some row has a masked key
+                    const int32_t keep = limit - t * BN - h * CW;
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c * 32 + j >= keep)
+                                sv[c][j] = kNegInf;
+                }
+                float mx = kNegInf;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c * 32 + j >= keep)
-                            sv[c][j] = kNegInf;
-            }
-            float mx = kNegInf;
+                    for (int j = 0; j < 32; j += 2)
+                        mx = max3(mx, sv[c][j], sv[c][j + 1]);
+                // The row's maximum over its HS warps (slots by tile parity);
+                // and P V of the tile before has read P and written O.
+                if constexpr (HS > 1)
+                    xmax[t & 1][x][h][r] = mx;
+                await(3 + x, &bar_pv[x], done + static_cast<uint32_t>(t - 1), t > 0);
+                tc_fence_after();
+                if constexpr (HS > 1) {
 #pragma unroll
-            for (int c = 0; c < NCH; ++c)
-#pragma unroll
-                for (int j = 0; j < 32; j += 2)
-                    mx = max3(mx, sv[c][j], sv[c][j + 1]);
-            // The row's maximum over its HS warps (slots by tile parity); and
-            // P V of the tile before has read P and written O.
-            if constexpr (HS > 1)
-                xmax[t & 1][x][h][r] = mx;
-            await(3 + x, smem_addr(&bar_pv[x]), static_cast<uint32_t>((t - 1) & 1), t > 0);
-            if constexpr (HS > 1) {
-#pragma unroll
-                for (int o = 0; o < HS; ++o)
-                    mx = fmaxf(mx, xmax[t & 1][x][o][r]);
-            }
-            // Lazy rescaling: the reference m (base 2) moves only when the
-            // tile's max exceeds it by more than 2^8; O / l and the logsumexp
-            // only need m and l to agree.
-            const float mx_s = mx * scale_log2;
-            float alpha = 1.0f;
-            if (mx_s > m + kLazyRescaleLog2) {
-                alpha = ex2_ftz(m - mx_s);
-                m = mx_s;
-            }
-            const float nref = m == kNegInf ? 0.0f : -m;
-            if (t > 0 && !__all_sync(0xffffffffu, alpha == 1.0f)) {
-#pragma unroll 1
-                for (int c = 0; c < OW; c += 8)
-                    tmem_scale8(t_row + o_col + c, alpha);
-            }
-            float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float p0, p1;
-                    fma2(p0, p1, sv[c][2 * j], sv[c][2 * j + 1], scale_log2, scale_log2, nref, nref);
-                    p0 = ex2_ftz(p0);
-                    p1 = ex2_ftz(p1);
-                    add2(sum0, sum1, sum0, sum1, p0, p1);
-                    w[j] = Elem<T>::pack2(p0, p1);
+                    for (int o = 0; o < HS; ++o)
+                        mx = fmaxf(mx, xmax[t & 1][x][o][r]);
                 }
-                tmem_st16(t_row + p_col + c * 16, w);
+                // Lazy rescaling: the reference m (base 2) moves only when the
+                // tile's max exceeds it by more than 2^8; O / l and the
+                // logsumexp only need m and l to agree.
+                const float mx_s = mx * scale_log2;
+                float alpha = 1.0f;
+                if (mx_s > m + kLazyRescaleLog2) {
+                    alpha = ex2_ftz(m - mx_s);
+                    m = mx_s;
+                }
+                const float nref = m == kNegInf ? 0.0f : -m;
+                if (t > 0 && !__all_sync(0xffffffffu, alpha == 1.0f)) {
+#pragma unroll 1
+                    for (int c = 0; c < OW; c += 8)
+                        tmem_scale8(t_row + o_col + c, alpha);
+                }
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float p0, p1;
+                        fma2(p0, p1, sv[c][2 * j], sv[c][2 * j + 1], scale_log2, scale_log2, nref,
+                             nref);
+                        p0 = ex2_ftz(p0);
+                        p1 = ex2_ftz(p1);
+                        add2(sum0, sum1, sum0, sum1, p0, p1);
+                        w[j] = Elem<T>::pack2(p0, p1);
+                    }
+                    tmem_st16(t_row + p_col + c * 16, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_leader<CG>(bar_weights);     // release: P written, O rescaled
+                l = l * alpha + (sum0 + sum1);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_leader<CG>(bar_weights);         // release: P written, O rescaled
-            l = l * alpha + (sum0 + sum1);
-        }
-        if (my_kt > 0)
-            await(1 + x, smem_addr(&bar_pv[x]), static_cast<uint32_t>((my_kt - 1) & 1), true);
-        if constexpr (HS > 1) {
-            xsum[x][h][r] = l;
-            named_barrier(pair_bar, 32 * HS);
-            l = 0.0f;
-#pragma unroll
-            for (int o = 0; o < HS; ++o)
-                l += xsum[x][o][r];
-        }
-        if (!__any_sync(0xffffffffu, failed_elsewhere()) && my_kt >= 0) {
-            const float inv = 1.0f / l;
-            unsigned short* const dst = static_cast<unsigned short*>(p.o.data) +
-                                        (u.q0 + static_cast<int64_t>(token)) * p.o.row +
-                                        head * p.o.head + h * OW;
-            // A masked key's weight is 0, but 0 times an infinite or NaN
-            // value of V is NaN: rows that came out so, and have such a value
-            // in the masked part of their key tiles, are done again over
-            // their visible keys alone (by the row's first warp, and before
-            // anything is stored there: o may be q).
+            // ---- O / l to global memory, logsumexp
             bool finite = true;
-            if (my_kt > 0) {                                 // warp-uniform, as tcgen05.ld needs
-#pragma unroll
+            if (my_kt > 0) {
+                await(1 + x, &bar_pv[x], done + static_cast<uint32_t>(my_kt - 1), true);
+                tc_fence_after();
+#pragma unroll 1
                 for (int c = 0; c < OW / 32; ++c) {
                     float ov[32];
                     tmem_ld32(t_row + o_col + c * 32, ov);
                     tmem_wait_ld();
+                    float big = 0.0f;                        // NaN is not passed over
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        finite = finite && fabsf(ov[j] * inv) < kInf;
+                        big = fmaxf(big, ov[j] - ov[j] == 0.0f ? 0.0f : 1.0f);
+                    finite = finite && big == 0.0f;
                 }
             }
-            unsigned redo = __ballot_sync(0xffffffffu, real && limit > 0 && !finite);
+            done += static_cast<uint32_t>(my_kt);
+            unsigned redo = __ballot_sync(0xffffffffu, !finite);
             if constexpr (HS > 1) {
+                xsum[x][h][r] = l;
                 if (lane == 0)
                     xredo[x][h][warp & 3] = redo;
                 named_barrier(pair_bar, 32 * HS);
+                l = 0.0f;
 #pragma unroll
-                for (int o = 0; o < HS; ++o)
+                for (int o = 0; o < HS; ++o) {
+                    l += xsum[x][o][r];
                     redo |= xredo[x][o][warp & 3];
+                }
+                named_barrier(pair_bar, 32 * HS);            // read before the next unit's
             }
+            // A masked key's weight is 0, but 0 times an infinite or NaN value
+            // of V is NaN: rows that came out so, and have such a value in the
+            // masked part of their key tiles, are done again over their
+            // visible keys alone (by the row's first warp, and before anything
+            // is stored there: o may be q).
+            const int kvh = u.head / group;
+            const bool broken = failed_elsewhere();          // then nothing is stored
+            redo &= __ballot_sync(0xffffffffu, token < u.n_q && limit > 0 && !broken);
             if (redo) {
                 const unsigned short* const v = static_cast<const unsigned short*>(p.v.data) +
                                                 static_cast<int64_t>(u.k0) * p.v.row +
@@ -690,43 +851,71 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                                                        redo >> lane & 1 ? limit : 0x7fffffff);
                 const int64_t to = min(static_cast<int64_t>(my_kt) * BN, p.total_k - u.k0);
                 bool hit = false;
-                for (int64_t i = static_cast<int64_t>(from) * (D / 2) + lane; i < to * (D / 2);
-                     i += 32) {
+                for (int64_t e = static_cast<int64_t>(from) * (D / 2) + lane; e < to * (D / 2);
+                     e += 32) {
                     float a, b;
                     Elem<T>::unpack2(__ldg(reinterpret_cast<const unsigned*>(
-                                         v + (i / (D / 2)) * p.v.row + (i % (D / 2)) * 2)), a, b);
+                                         v + (e / (D / 2)) * p.v.row + (e % (D / 2)) * 2)), a, b);
                     hit = hit || !(fabsf(a) < kInf) || !(fabsf(b) < kInf);
                 }
                 if (!__any_sync(0xffffffffu, hit))
                     redo = 0;
             }
-            const bool store = real && !(redo >> lane & 1);
             // A row that sees no key is the softmax of only -inf: NaN.
-            const float nan = __int_as_float(0x7fc00000);
-#pragma unroll
+            const float inv = limit > 0 ? 1.0f / l : __int_as_float(0x7fc00000);
+            const unsigned rows = __ballot_sync(0xffffffffu, token < u.n_q && !broken) & ~redo;
+            unsigned short* const dst = static_cast<unsigned short*>(p.o.data) + h * OW;
+#pragma unroll 1
             for (int c = 0; c < OW / 32; ++c) {
                 float ov[32];
-                if (my_kt > 0) {
-                    tmem_ld32(t_row + o_col + c * 32, ov);
-                    tmem_wait_ld();
+                tmem_ld32(t_row + o_col + c * 32, ov);       // (no key tile: anything, times NaN)
+                tmem_wait_ld();
+                if (c + 1 == OW / 32 && my_kt > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_leader<CG>(bar_output);  // O may be overwritten
                 }
-                if (store) {
+                // EC columns of 32 rows at a time through shared memory (their
+                // 16-byte chunks XOR-swizzled so that eight rows fill the
+                // banks), so that a store covers whole sectors of 16 or 8 rows.
+                constexpr int CH = EC / 8;                   // chunks of a staged row
+                auto staged = [&](int row, int chunk) {
+                    return stage + static_cast<uint32_t>(row * EC * 2) +
+                           ((chunk ^ ((row / (8 / CH)) % CH)) << 4);
+                };
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        ov[j] = limit > 0 ? ov[j] * inv : nan;
+                for (int e = 0; e < 32; e += EC) {
+                    __syncwarp();
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
+                    for (int g = 0; g < CH; ++g) {
+                        const float* f = ov + e + g * 8;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     :: "r"(staged(lane, g)),
+                                        "r"(Elem<T>::pack2(f[0] * inv, f[1] * inv)),
+                                        "r"(Elem<T>::pack2(f[2] * inv, f[3] * inv)),
+                                        "r"(Elem<T>::pack2(f[4] * inv, f[5] * inv)),
+                                        "r"(Elem<T>::pack2(f[6] * inv, f[7] * inv)) : "memory");
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < CH; ++g) {
+                        const int q = g * (32 / CH) + lane / CH, chunk = lane % CH;
                         uint4 w;
-                        w.x = Elem<T>::pack2(ov[g * 8 + 0], ov[g * 8 + 1]);
-                        w.y = Elem<T>::pack2(ov[g * 8 + 2], ov[g * 8 + 3]);
-                        w.z = Elem<T>::pack2(ov[g * 8 + 4], ov[g * 8 + 5]);
-                        w.w = Elem<T>::pack2(ov[g * 8 + 6], ov[g * 8 + 7]);
-                        *reinterpret_cast<uint4*>(dst + c * 32 + g * 8) = w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(staged(q, chunk)) : "memory");
+                        const int row = (warp & 3) * 32 + q;
+                        const int64_t qrow = u.q0 + static_cast<int64_t>(first + (row >> gp_log2));
+                        if (rows >> q & 1)
+                            *reinterpret_cast<uint4*>(dst + qrow * p.o.row +
+                                                      (u.head + (row & (gp - 1))) * p.o.head +
+                                                      c * 32 + e + chunk * 8) = w;
                     }
                 }
             }
-            if (p.lse && store && h == 0)
-                p.lse[(u.q0 + static_cast<int64_t>(token)) * p.n_heads + head] =
+            if (p.lse && h == 0 && (rows >> lane & 1))
+                p.lse[(u.q0 + static_cast<int64_t>(token)) * p.n_heads + u.head + (r & (gp - 1))] =
                     limit > 0 && l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
             while (redo && h == 0) {
                 const int row = (warp & 3) * 32 + __ffs(redo) - 1;

@@ -177,4 +177,34 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
             : "memory");
 }
 
+// Cluster launch control (sm_100): ask for a cluster of this grid that has not
+// been launched yet, in its place.  The 16-byte answer arrives in both CTAs
+// at this offset, with 16 bytes on the barrier at the other.
+template <int CG>
+__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar)
+{
+    if constexpr (CG == 1)
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta"
+                     ".mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                     :: "r"(answer), "r"(bar) : "memory");
+    else
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta"
+                     ".mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];"
+                     :: "r"(answer), "r"(bar) : "memory");
+}
+
+// blockIdx.x of the first CTA of the cluster that an answer gave, -1 when it
+// gave none (no cluster is left; nothing may be asked for after that).
+__device__ __forceinline__ int64_t clc_first_cta(uint32_t answer)
+{
+    uint32_t given, x;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+                 "ld.shared.b128 r, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                 : "=r"(given), "=r"(x) : "r"(answer) : "memory");
+    return given ? static_cast<int64_t>(x) : -1;
+}
+
 }  // namespace rwsm

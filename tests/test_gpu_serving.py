@@ -178,6 +178,39 @@ def test_packed(i, dtype):
     packed_case(n_q, n_k, h, hk, d, causal, dtype, 200 + i, fused)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_many_units_per_cta(d, causal):
+    """Several times more units of work than fit on the device, with query
+    tiles that end at different key tiles (or have no rows), checked head by
+    head against float64 on the device."""
+    r = np.random.default_rng(17)
+    n_q = [int(x) for x in r.integers(1, 900, 40)] + [0, 1, 513, 257]
+    n_k = [n + int(r.integers(-60, 300)) if n > 100 else n for n in n_q]
+    h, hk, dtype = 16, 16, torch.bfloat16
+    g = rng(61)
+    q = normal(g, sum(n_q), h, d, dtype=dtype, by=1.5)
+    k, v = (normal(g, sum(n_k), hk, d, dtype=dtype) for _ in range(2))
+    cu_q, cu_k = np.cumsum([0] + n_q), np.cumsum([0] + n_k)
+    for _ in range(3):
+        o = rws.attention_packed(q, k, v, ints(cu_q), ints(cu_k), causal=causal)
+    assert rws.device_status() == rws.OK
+    for s in range(len(n_q)):
+        a, b, c, e = cu_q[s], cu_q[s + 1], cu_k[s], cu_k[s + 1]
+        qs, ks, vs = (x.double().transpose(0, 1) for x in (q[a:b], k[c:e], v[c:e]))
+        z = qs @ ks.transpose(1, 2) * d ** -0.5
+        if causal:
+            i, j = torch.arange(b - a, device="cuda"), torch.arange(e - c, device="cuda")
+            z.masked_fill_(j[None] > i[:, None] + (e - c) - (b - a), float("-inf"))
+        w = torch.softmax(z, -1)
+        want, mag = ((w @ x).transpose(0, 1) for x in (vs, vs.abs()))
+        got = o[a:b].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        bound = (2.0 ** -8 + 2.0 ** -14) * mag + 2.0 ** -8 * want.abs() + 2.0 ** -24
+        fine = ~torch.isnan(want)
+        assert bool(((got - want).abs()[fine] <= bound[fine]).all()), (s, n_q[s], n_k[s])
+
+
 # ---------------------------------------------------------------- append
 def append_case(n, h, hk, d, rot, interleaved, page, dtype, seed, far=5000, positions=None,
                 seq_ids=None, n_seqs=None, in_place=False):
