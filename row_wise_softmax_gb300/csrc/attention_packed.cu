@@ -178,22 +178,24 @@ struct Unit {
     int32_t ok;
 };
 
-// Number of sequence s's units that visit at least x key tiles (x >= 1), and
-// through `first` the first of them.
-__device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int32_t tokens, int bn,
-                                              bool causal, int32_t x, int32_t& first)
+// Number of a sequence's units (of 2^tok_log2 query tokens) that visit at least
+// x key tiles of BN keys, and through `first` the first of them.
+template <int BN>
+__device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int tok_log2, bool causal,
+                                              int32_t x, int32_t& first)
 {
-    const int32_t units = (n_q + tokens - 1) / tokens;
+    const int32_t last = (1 << tok_log2) - 1;
+    const int32_t units = static_cast<int32_t>((static_cast<uint32_t>(n_q) + last) >> tok_log2);
     first = 0;
     if (x <= 0)
         return units;
-    if (units == 0 || x > (n_k + bn - 1) / bn)
+    if (units == 0 || (x - 1) * static_cast<int64_t>(BN) >= n_k)
         return 0;
     if (causal) {
-        // Unit i's last query min((i + 1) tokens, n_q) - 1 sees key (x - 1) bn.
-        const int64_t need = static_cast<int64_t>(x - 1) * bn - (n_k - n_q) + 1;
-        if (need > tokens)
-            first = static_cast<int32_t>((need + tokens - 1) / tokens) - 1;
+        // Unit i's last query min((i + 1) tokens, n_q) - 1 sees key (x - 1) BN.
+        const int64_t need = static_cast<int64_t>(x - 1) * BN - (n_k - n_q) + 1;
+        if (need > last + 1)
+            first = static_cast<int32_t>((need + last) >> tok_log2) - 1;
         if (first > units - 1)
             first = units - 1;
     }
@@ -207,6 +209,7 @@ __device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int32_t 
 // and the walk goes on from where the last one ended.
 constexpr int kRanked = 128;
 
+template <int BN>
 struct UnitFinder {
     int32_t q0[4], n_q[4], k0[4], n_k[4];
     int32_t most;                                  // most key tiles of a unit
@@ -225,17 +228,16 @@ struct UnitFinder {
     }
 
     // Units that visit at least x key tiles.
-    __device__ __forceinline__ int32_t count(const PackedProblem& p, int32_t tokens, int bn,
-                                             int32_t x) const
+    __device__ __forceinline__ int32_t count(const PackedProblem& p, int tok_log2, int32_t x) const
     {
         int32_t n = 0, first;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            n += units_with(n_q[i], n_k[i], tokens, bn, p.causal, x, first);
+            n += units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, x, first);
         return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
     }
 
-    __device__ void init(const PackedProblem& p, int32_t tokens, int bn, bool report)
+    __device__ void init(const PackedProblem& p, int tok_log2, bool report)
     {
         const int lane = threadIdx.x & 31;
         at = before = 0;
@@ -249,10 +251,10 @@ struct UnitFinder {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             lengths(p, i * 32 + lane, i, report);
-            longest = n_q[i] > 0 ? max(longest, (n_k[i] + bn - 1) / bn) : longest;
+            longest = n_q[i] > 0 ? max(longest, static_cast<int32_t>((n_k[i] + BN - 1u) / BN)) : longest;
         }
         most = __reduce_max_sync(0xffffffffu, longest);
-        total = count(p, tokens, bn, 0);
+        total = count(p, tok_log2, 0);
     }
 
     // The first of the 32 sequences in slot i whose units, n to a lane, hold
@@ -291,7 +293,7 @@ struct UnitFinder {
         return u;
     }
 
-    __device__ Unit find(const PackedProblem& p, int64_t rank, int32_t tokens, int bn)
+    __device__ Unit find(const PackedProblem& p, int64_t rank, int tok_log2)
     {
         const int lane = threadIdx.x & 31;
         Unit none = {};
@@ -304,7 +306,8 @@ struct UnitFinder {
             for (; at < p.n_seqs; at += 32) {
                 lengths(p, at + lane, 0, false);
                 int64_t left = rank - before;
-                const int32_t n = (n_q[0] + tokens - 1) / tokens;
+                int32_t first;
+                const int32_t n = units_with<BN>(n_q[0], n_k[0], tok_log2, p.causal, 0, first);
                 const int l = pick(n, left, passed);
                 if (l >= 0)                        // longest first within the sequence
                     return unit(0, l, __shfl_sync(0xffffffffu, n, l) - 1 -
@@ -317,7 +320,7 @@ struct UnitFinder {
         }
         int32_t lo = 0, hi = most + 1, above = 0;  // count(lo) > rank >= count(hi) = above
         while (lo + 1 < hi) {
-            const int32_t x = lo + (hi - lo) / 2, n = count(p, tokens, bn, x);
+            const int32_t x = lo + (hi - lo) / 2, n = count(p, tok_log2, x);
             if (n > rank) {
                 lo = x;
             } else {
@@ -329,8 +332,8 @@ struct UnitFinder {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             int32_t first, next;
-            int32_t n = units_with(n_q[i], n_k[i], tokens, bn, p.causal, lo, first);
-            n -= units_with(n_q[i], n_k[i], tokens, bn, p.causal, lo + 1, next);
+            int32_t n = units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, lo, first);
+            n -= units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, lo + 1, next);
             const int l = pick(n, left, passed);
             if (l >= 0)
                 return unit(i, l, __shfl_sync(0xffffffffu, first, l) + static_cast<int32_t>(left));
@@ -463,17 +466,32 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         // its columns of V; all complete on the even CTA's barriers, where
         // the bytes of both are announced.
         const bool one = lane == 0;
-        const int64_t blocks = p.n_heads >> gp_log2;
-        UnitFinder finder;
-        finder.init(p, tokens, BN, blockIdx.x == 0);
-        int64_t index = blockIdx.x / CG;
+        const int tok_log2 = 8 + (CG - 1) - gp_log2;
+        const uint32_t blocks = static_cast<uint32_t>(p.n_heads) >> gp_log2;
+        UnitFinder<BN> finder;
+        finder.init(p, tok_log2, blockIdx.x == 0);
+        auto find = [&](uint32_t cta) {
+            const uint32_t index = cta / CG, unit = index / blocks;
+            Unit u = finder.find(p, unit, tok_log2);
+            u.head = static_cast<int32_t>((index - unit * blocks) << gp_log2);
+            return u;
+        };
         uint32_t kv = 0, q_uses = 0;
         auto announce = [&](unsigned long long* bar, uint32_t bytes) {
             if (one && rank == 0)
                 mbar_arrive_expect_tx(smem_addr(bar), bytes * CG);
             return leader_addr<CG>(smem_addr(bar));
         };
-        for (uint32_t i = 0; index >= 0 && !failed; ++i) {
+        Unit u = find(blockIdx.x);
+        for (uint32_t i = 0; !failed; ++i) {
+            if (i >= 2)
+                wait1(&unit_free[i & 1], (i - 2) >> 1);
+            if (one) {
+                s_unit[i & 1] = u;
+                mbar_arrive(smem_addr(&unit_full[i & 1]));
+            }
+            if (u.ok < 0)
+                break;                                       // no unit is left, and all know
             // Ask for the next unit: the answer of two units ago has been
             // read by both CTAs.
             if (one)
@@ -484,17 +502,10 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 if (one)
                     clc_try_cancel<CG>(smem_addr(&s_next[i & 1]), smem_addr(&next_full[i & 1]));
             }
-            Unit u = finder.find(p, index / blocks, tokens, BN);
-            u.head = static_cast<int32_t>(index % blocks) << gp_log2;
-            if (i >= 2)
-                wait1(&unit_free[i & 1], (i - 2) >> 1);
-            if (one) {
-                s_unit[i & 1] = u;
-                mbar_arrive(smem_addr(&unit_full[i & 1]));
-            }
             const int32_t n_kt = max(tiles_of(u, 0), tiles_of(u, 1));
+            const int kvh = u.head / group;
+            Unit next = {};
             if (n_kt > 0) {
-                const int kvh = u.head / group;
                 if (q_uses > 0)
                     wait1(&q_free, q_uses - 1);
                 ++q_uses;
@@ -508,7 +519,9 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                                             u.head, u.q0 + u.tile * tokens +
                                             (x * CG + static_cast<int>(rank)) * tile_tokens, bar_q);
                 }
-                for (int32_t t = 0; t < n_kt && !failed; ++t, ++kv) {
+            }
+            for (int32_t t = 0; t < max(n_kt, 1) && !failed; ++t) {
+                if (t < n_kt) {
                     if (kv >= KVS)
                         wait1(&k_free[slot(kv)], (kv - KVS) / KVS);          // every S done
                     const uint32_t bar_k = announce(&k_full[slot(kv)], KV_BYTES);
@@ -525,33 +538,31 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     if (one && !failed)
                         tma_load_3d<CG>(sV + slot(kv) * KV_BYTES, &map_v,
                                         static_cast<int>(rank) * VD, kvh, u.k0 + t * BN, bar_v);
-                    if (failed_elsewhere())
-                        failed = true;
+                    ++kv;
                 }
-            }
-            // The answer; both CTAs get the same.
-            const bool answered =
-                __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&next_full[i & 1]), (i >> 1) & 1u));
-            int64_t next = -1;
-            if (answered)
-                next = clc_first_cta(smem_addr(&s_next[i & 1]));
-            else
-                fail();
-            fence_proxy_async_smem();                        // read before it is written again
-            __syncwarp();
-            if (one)
-                mbar_arrive_leader<CG>(leader_addr<CG>(smem_addr(&next_free[i & 1])));
-            index = next < 0 ? -1 : next / CG;
-            if (index < 0) {
-                // No unit is left: say so.
-                ++i;
-                if (i >= 2)
-                    wait1(&unit_free[i & 1], (i - 2) >> 1);
-                if (one) {
-                    s_unit[i & 1].ok = -1;
-                    mbar_arrive(smem_addr(&unit_full[i & 1]));
+                // The answer (both CTAs get the same), and which unit that
+                // is, while the ring is full and long before it is wanted.
+                if (t == min(KVS, max(n_kt, 1)) - 1) {
+                    const bool answered = __all_sync(
+                        0xffffffffu, mbar_wait_bounded(smem_addr(&next_full[i & 1]), (i >> 1) & 1u));
+                    int64_t cta = -1;
+                    if (answered)
+                        cta = clc_first_cta(smem_addr(&s_next[i & 1]));
+                    else
+                        fail();
+                    fence_proxy_async_smem();                // read before it is written again
+                    __syncwarp();
+                    if (one)
+                        mbar_arrive_leader<CG>(leader_addr<CG>(smem_addr(&next_free[i & 1])));
+                    if (cta >= 0)
+                        next = find(static_cast<uint32_t>(cta));
+                    else
+                        next.ok = -1;
                 }
+                if (failed_elsewhere())
+                    failed = true;
             }
+            u = next;
         }
         if (rank == 0 && failed_elsewhere()) {
             // Let the copies still in flight land (bounded; after one wait
@@ -804,67 +815,104 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 l = l * alpha + (sum0 + sum1);
             }
             // ---- O / l to global memory, logsumexp
-            bool finite = true;
             if (my_kt > 0) {
                 await(1 + x, &bar_pv[x], done + static_cast<uint32_t>(my_kt - 1), true);
                 tc_fence_after();
+            }
+            done += static_cast<uint32_t>(my_kt);
+            if constexpr (HS > 1) {
+                xsum[x][h][r] = l;
+                named_barrier(pair_bar, 32 * HS);
+                l = 0.0f;
+#pragma unroll
+                for (int o = 0; o < HS; ++o)
+                    l += xsum[x][o][r];
+            }
+            // A masked key's weight is 0, but 0 times an infinite or NaN value
+            // of V is NaN.  Rows with a value of O that is not finite, and
+            // such a value in the masked part of their key tiles, are done
+            // again over their visible keys alone, after the others have been
+            // stored; where o is q, nothing may be stored in them before.
+            const bool in_place = p.o.data == p.q.data;
+            float zero0 = 0.0f, zero1 = 0.0f;                // 0 * O: NaN unless O is finite
+            auto add_zeros = [&](const float (&v)[32]) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    fma2(zero0, zero1, v[j], v[j + 1], 0.0f, 0.0f, zero0, zero1);
+            };
+            if (in_place && my_kt > 0) {
 #pragma unroll 1
                 for (int c = 0; c < OW / 32; ++c) {
                     float ov[32];
                     tmem_ld32(t_row + o_col + c * 32, ov);
                     tmem_wait_ld();
-                    float big = 0.0f;                        // NaN is not passed over
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        big = fmaxf(big, ov[j] - ov[j] == 0.0f ? 0.0f : 1.0f);
-                    finite = finite && big == 0.0f;
+                    add_zeros(ov);
                 }
             }
-            done += static_cast<uint32_t>(my_kt);
-            unsigned redo = __ballot_sync(0xffffffffu, !finite);
-            if constexpr (HS > 1) {
-                xsum[x][h][r] = l;
-                if (lane == 0)
-                    xredo[x][h][warp & 3] = redo;
-                named_barrier(pair_bar, 32 * HS);
-                l = 0.0f;
-#pragma unroll
-                for (int o = 0; o < HS; ++o) {
-                    l += xsum[x][o][r];
-                    redo |= xredo[x][o][warp & 3];
-                }
-                named_barrier(pair_bar, 32 * HS);            // read before the next unit's
-            }
-            // A masked key's weight is 0, but 0 times an infinite or NaN value
-            // of V is NaN: rows that came out so, and have such a value in the
-            // masked part of their key tiles, are done again over their
-            // visible keys alone (by the row's first warp, and before anything
-            // is stored there: o may be q).
-            const int kvh = u.head / group;
             const bool broken = failed_elsewhere();          // then nothing is stored
-            redo &= __ballot_sync(0xffffffffu, token < u.n_q && limit > 0 && !broken);
-            if (redo) {
-                const unsigned short* const v = static_cast<const unsigned short*>(p.v.data) +
-                                                static_cast<int64_t>(u.k0) * p.v.row +
-                                                kvh * p.v.head;
-                const int32_t from = __reduce_min_sync(0xffffffffu,
-                                                       redo >> lane & 1 ? limit : 0x7fffffff);
-                const int64_t to = min(static_cast<int64_t>(my_kt) * BN, p.total_k - u.k0);
-                bool hit = false;
-                for (int64_t e = static_cast<int64_t>(from) * (D / 2) + lane; e < to * (D / 2);
-                     e += 32) {
-                    float a, b;
-                    Elem<T>::unpack2(__ldg(reinterpret_cast<const unsigned*>(
-                                         v + (e / (D / 2)) * p.v.row + (e % (D / 2)) * 2)), a, b);
-                    hit = hit || !(fabsf(a) < kInf) || !(fabsf(b) < kInf);
+            const unsigned seen = __ballot_sync(0xffffffffu, token < u.n_q && limit > 0 && !broken);
+            unsigned rows = __ballot_sync(0xffffffffu, token < u.n_q && !broken);
+            // The rows that any of the HS warps found not finite.
+            auto not_finite = [&] {
+                unsigned redo = __ballot_sync(0xffffffffu, !(zero0 + zero1 == 0.0f)) & seen;
+                if constexpr (HS > 1) {
+                    if (lane == 0)
+                        xredo[x][h][warp & 3] = redo;
+                    named_barrier(pair_bar, 32 * HS);
+#pragma unroll
+                    for (int o = 0; o < HS; ++o)
+                        redo |= xredo[x][o][warp & 3];
+                    named_barrier(pair_bar, 32 * HS);        // read before it is written again
                 }
-                if (!__any_sync(0xffffffffu, hit))
-                    redo = 0;
+                return redo;
+            };
+            const int kvh = u.head / group;
+            // Of those, the ones with such a V in the masked part.
+            auto leaked = [&](unsigned redo) {
+                if (redo) {
+                    const unsigned short* const v = static_cast<const unsigned short*>(p.v.data) +
+                                                    static_cast<int64_t>(u.k0) * p.v.row +
+                                                    kvh * p.v.head;
+                    const int32_t from = __reduce_min_sync(0xffffffffu,
+                                                           redo >> lane & 1 ? limit : 0x7fffffff);
+                    const int64_t to = min(static_cast<int64_t>(my_kt) * BN, p.total_k - u.k0);
+                    bool hit = false;
+                    for (int64_t e = static_cast<int64_t>(from) * (D / 2) + lane; e < to * (D / 2);
+                         e += 32) {
+                        float a, b;
+                        Elem<T>::unpack2(__ldg(reinterpret_cast<const unsigned*>(
+                                             v + (e / (D / 2)) * p.v.row + (e % (D / 2)) * 2)),
+                                         a, b);
+                        hit = hit || !(fabsf(a) < kInf) || !(fabsf(b) < kInf);
+                    }
+                    if (!__any_sync(0xffffffffu, hit))
+                        redo = 0;
+                }
+                return redo;
+            };
+            unsigned redo = 0;
+            if (in_place) {
+                redo = leaked(not_finite());
+                rows &= ~redo;
             }
             // A row that sees no key is the softmax of only -inf: NaN.
             const float inv = limit > 0 ? 1.0f / l : __int_as_float(0x7fc00000);
-            const unsigned rows = __ballot_sync(0xffffffffu, token < u.n_q && !broken) & ~redo;
-            unsigned short* const dst = static_cast<unsigned short*>(p.o.data) + h * OW;
+            // EC columns of 32 rows at a time go through shared memory (their
+            // 16-byte chunks XOR-swizzled so that eight rows fill the banks),
+            // so that a store covers whole sectors of several rows.
+            constexpr int CH = EC / 8;                       // chunks of a staged row
+            auto staged = [&](int row, int chunk) {
+                return stage + static_cast<uint32_t>(row * EC * 2) +
+                       ((chunk ^ ((row / (8 / CH)) % CH)) << 4);
+            };
+            unsigned short* dst[CH];                         // this lane's place in CH of the rows
+#pragma unroll
+            for (int g = 0; g < CH; ++g) {
+                const int row = (warp & 3) * 32 + g * (32 / CH) + lane / CH;
+                dst[g] = static_cast<unsigned short*>(p.o.data) +
+                         (u.q0 + static_cast<int64_t>(first + (row >> gp_log2))) * p.o.row +
+                         (u.head + (row & (gp - 1))) * p.o.head + h * OW + lane % CH * 8;
+            }
 #pragma unroll 1
             for (int c = 0; c < OW / 32; ++c) {
                 float ov[32];
@@ -876,14 +924,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     if (lane == 0)
                         mbar_arrive_leader<CG>(bar_output);  // O may be overwritten
                 }
-                // EC columns of 32 rows at a time through shared memory (their
-                // 16-byte chunks XOR-swizzled so that eight rows fill the
-                // banks), so that a store covers whole sectors of 16 or 8 rows.
-                constexpr int CH = EC / 8;                   // chunks of a staged row
-                auto staged = [&](int row, int chunk) {
-                    return stage + static_cast<uint32_t>(row * EC * 2) +
-                           ((chunk ^ ((row / (8 / CH)) % CH)) << 4);
-                };
+                add_zeros(ov);
 #pragma unroll
                 for (int e = 0; e < 32; e += EC) {
                     __syncwarp();
@@ -900,20 +941,18 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < CH; ++g) {
-                        const int q = g * (32 / CH) + lane / CH, chunk = lane % CH;
+                        const int q = g * (32 / CH) + lane / CH;
                         uint4 w;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(staged(q, chunk)) : "memory");
-                        const int row = (warp & 3) * 32 + q;
-                        const int64_t qrow = u.q0 + static_cast<int64_t>(first + (row >> gp_log2));
+                                     : "r"(staged(q, lane % CH)) : "memory");
                         if (rows >> q & 1)
-                            *reinterpret_cast<uint4*>(dst + qrow * p.o.row +
-                                                      (u.head + (row & (gp - 1))) * p.o.head +
-                                                      c * 32 + e + chunk * 8) = w;
+                            *reinterpret_cast<uint4*>(dst[g] + c * 32 + e) = w;
                     }
                 }
             }
+            if (!in_place)
+                redo = leaked(not_finite());
             if (p.lse && h == 0 && (rows >> lane & 1))
                 p.lse[(u.q0 + static_cast<int64_t>(token)) * p.n_heads + u.head + (r & (gp - 1))] =
                     limit > 0 && l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
