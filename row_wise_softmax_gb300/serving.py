@@ -12,8 +12,8 @@ allocated for that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -22,20 +22,11 @@ from . import BF16, F16, OK, SoftmaxError, lib
 __all__ = ["kv_append", "attention_packed", "attention_decode"]
 
 _CODES = {torch.bfloat16: BF16, torch.float16: F16}
-_i64, _vp = ctypes.c_int64, ctypes.c_void_p
 
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("row_stride", _i64), ("head_stride", _i64)]
-
-
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", _vp), ("v", _vp), ("n_pages", _i64), ("page_size", _i64),
-                ("n_kv_heads", _i64), ("head_dim", _i64), ("k_page_stride", _i64),
-                ("k_row_stride", _i64), ("k_head_stride", _i64), ("v_page_stride", _i64),
-                ("v_row_stride", _i64), ("v_head_stride", _i64), ("page_table", _vp),
-                ("n_seqs", _i64), ("table_width", _i64), ("table_stride", _i64)]
-
+# softmax_heads_t and softmax_paged_cache_t, packed: the calls of one decoding
+# step are short, and building ctypes structures costs more than they do.
+_HEADS = struct.Struct("=Qqq").pack
+_CACHE = struct.Struct("=QQ10qQ3q").pack
 
 _declared = None
 
@@ -45,80 +36,94 @@ def _lib():
     global _declared
     if _declared is None:
         L = lib()
-        hp, cp, ci = ctypes.POINTER(_Heads), ctypes.POINTER(_Cache), ctypes.c_int
-        cf = ctypes.c_float
-        L.softmax_kv_append.argtypes = [cp, hp, hp, hp, hp, _i64, _vp, _vp, _i64, _vp, _i64, ci,
-                                        ci, _vp]
+        i64, vp, ci, cf, sp = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
+                               ctypes.c_char_p)            # sp: a packed structure
+        L.softmax_kv_append.argtypes = [sp, sp, sp, sp, sp, i64, vp, vp, i64, vp, i64, ci, ci, vp]
         L.softmax_kv_append.restype = ci
-        L.softmax_attention_decode.argtypes = [cp, hp, hp, _vp, _i64, _vp, cf, ci, _vp,
-                                               ctypes.c_size_t, _vp]
+        L.softmax_attention_decode.argtypes = [sp, sp, sp, vp, i64, vp, cf, ci, vp,
+                                               ctypes.c_size_t, vp]
         L.softmax_attention_decode.restype = ci
-        L.softmax_attention_decode_workspace.argtypes = [_i64] * 5
-        L.softmax_attention_decode_workspace.restype = _i64
-        L.softmax_attention_packed.argtypes = [hp, hp, hp, hp, _vp, _vp, _vp, _i64, _i64, _i64,
-                                               _i64, _i64, _i64, cf, ci, ci, _vp]
+        L.softmax_attention_decode_workspace.argtypes = [i64] * 5
+        L.softmax_attention_decode_workspace.restype = i64
+        L.softmax_attention_packed.argtypes = [sp, sp, sp, sp, vp, vp, vp, i64, i64, i64, i64, i64,
+                                               i64, cf, ci, ci, vp]
         L.softmax_attention_packed.restype = ci
         _declared = L
     return _declared
 
 
-def _check(name, ref, **tensors):
-    """The dtype code of ``ref``, after checking that every tensor lies on its
-    device, shares its dtype and has contiguous head elements."""
-    code = _CODES.get(ref.dtype)
-    if code is None:
-        raise TypeError("%s: dtype must be bfloat16 or float16, got %s" % (name, ref.dtype))
-    for key, t in tensors.items():
-        if not t.is_cuda or t.device != ref.device:
-            raise ValueError("%s: %s must be a CUDA tensor on %s" % (name, key, ref.device))
-        if t.dtype != ref.dtype:
-            raise ValueError("%s: %s must have dtype %s" % (name, key, ref.dtype))
-        if t.stride(-1) != 1:
-            raise ValueError("%s: %s must have contiguous head elements" % (name, key))
-    return code
+def _same(name, key, t, dtype, device) -> None:
+    """t lies on CUDA device `device`, has dtype, and contiguous head elements."""
+    if t.get_device() != device:
+        raise ValueError("%s: %s must be a tensor on cuda:%d" % (name, key, device))
+    if t.dtype is not dtype:
+        raise ValueError("%s: %s must have dtype %s" % (name, key, dtype))
 
 
-def _index(name, key, t, shape, device):
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape:
-        raise ValueError("%s: %s must be an int32 tensor of shape %s on %s" %
-                         (name, key, list(shape), device))
-    if t.dim() and t.numel() > 1 and t.stride(-1) != 1:
-        raise ValueError("%s: %s must be contiguous" % (name, key))
+def _heads(name, key, t, dtype, device):
+    """softmax_heads_t of a [rows, heads, head_dim] tensor."""
+    _same(name, key, t, dtype, device)
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError("%s: %s must have contiguous head elements" % (name, key))
+    return _HEADS(t.data_ptr(), row, head)
+
+
+def _index(name, key, t, n, device):
+    """The address of an int32 vector of n elements."""
+    if t.dtype is not torch.int32 or t.get_device() != device or t.shape != (n,) or \
+            (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: %s must be a contiguous int32 tensor of shape [%d] on cuda:%d" %
+                         (name, key, n, device))
     return t.data_ptr()
 
 
-def _heads(t):
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _cache(name, k_cache, v_cache, page_table, n_seqs):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+def _cache(name, k, v, table, dtype, device):
+    """softmax_paged_cache_t of two caches and a page table."""
+    _same(name, "k_cache", k, dtype, device)
+    _same(name, "v_cache", v, dtype, device)
+    if k.dim() != 4 or k.shape != v.shape:
         raise ValueError("%s: k_cache and v_cache must be [pages, page_size, kv_heads, head_dim]"
                          % name)
-    if page_table.dim() != 2:
-        raise ValueError("%s: page_table must be [sequences, pages]" % name)
-    rows = page_table.shape[0] if n_seqs is None else n_seqs
-    width = page_table.shape[1]
-    _index(name, "page_table", page_table, (rows, width), k_cache.device)
-    p, r, h, d = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), p, r, h, d, ks[0], ks[1], ks[2], vs[0],
-                  vs[1], vs[2], page_table.data_ptr(), rows, width,
-                  page_table.stride(0) if rows > 1 else width)
+    if table.dtype is not torch.int32 or table.get_device() != device or table.dim() != 2:
+        raise ValueError("%s: page_table must be an int32 tensor [sequences, pages] on cuda:%d" %
+                         (name, device))
+    pages, size, heads, dim = k.shape
+    rows, width = table.shape
+    kp, kr, kh, k1 = k.stride()
+    vp, vr, vh, v1 = v.stride()
+    step, t1 = table.stride()
+    if k1 != 1 or v1 != 1 or (width > 1 and t1 != 1):
+        raise ValueError("%s: the caches' head elements and the table's rows must be contiguous"
+                         % name)
+    return _CACHE(k.data_ptr(), v.data_ptr(), pages, size, heads, dim, kp, kr, kh, vp, vr, vh,
+                  table.data_ptr(), rows, width, step if rows > 1 else width)
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The handle of ``stream`` (a torch stream, a raw handle, or None: the
-    current one), with its device current and allocations made for it."""
+def _device_of(name, t):
+    """t's CUDA device index and the dtype code of its dtype."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: dtype must be bfloat16 or float16, got %s" % (name, t.dtype))
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("%s: expects CUDA tensors" % name)
+    return device, code
+
+
+def _on(device, stream, run):
+    """run(handle) on ``stream`` (a torch stream, a raw handle, or None: the
+    device's current one), with its device current and allocations made for
+    it.  Returns what run returns."""
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return run(torch._C._cuda_getCurrentRawStream(device))
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+            return run(torch.cuda.current_stream(device).cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return run(stream.cuda_stream)
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=None, q_out=None,
@@ -143,48 +148,43 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
     if k.dim() != 3 or k.shape != v.shape:
         raise ValueError("kv_append: k and v must be [tokens, kv_heads, head_dim]")
     n, hk, d = k.shape
-    code = _check(name, k, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
-    device = k.device
-    cache = _cache(name, k_cache, v_cache, page_table, None)
-    if cache.n_kv_heads != hk or cache.head_dim != d:
+    device, code = _device_of(name, k)
+    dtype = k.dtype
+    cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
+    if k_cache.shape[2:] != (hk, d):
         raise ValueError("kv_append: the cache's heads do not match k")
-    pos = _index(name, "positions", positions, (n,), device)
+    ks, vs = _heads(name, "k", k, dtype, device), _heads(name, "v", v, dtype, device)
+    pos = _index(name, "positions", positions, n, device)
     if seq_ids is not None:
-        ids = _index(name, "seq_ids", seq_ids, (n,), device)
+        ids = _index(name, "seq_ids", seq_ids, n, device)
     else:
         ids = None
-        if cache.n_seqs < n:
+        if page_table.shape[0] < n:
             raise ValueError("kv_append: page_table has fewer rows than there are tokens")
     rot, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.device != device or inv_freq.dim() != 1 \
-                or not inv_freq.is_contiguous():
-            raise ValueError("kv_append: inv_freq must be a float64 vector on %s" % device)
-        rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    if q is None:
-        if q_out is not None:
-            raise ValueError("kv_append: q_out without q")
-    elif q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
-        raise ValueError("kv_append: q must be [tokens, heads, head_dim]")
-    else:
-        _check(name, k, q=q)
-        if q_out is not None:
-            _check(name, k, q_out=q_out)
-            if q_out.shape != q.shape:
-                raise ValueError("kv_append: q_out must match q")
-    with _on(device, stream) as handle:
-        if q is None:
-            qs = qo = None
-            h = 0
-        else:
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-            qs, qo, h = _heads(q), _heads(q_out), q.shape[1]
-        st = _lib().softmax_kv_append(cache, _heads(k), _heads(v), qs, qo, h, pos, ids, n, freq,
-                                     rot, 1 if interleaved else 0, code, handle)
-    if st != OK:
-        raise SoftmaxError(st, name)
-    return q_out
+        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != device or \
+                inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("kv_append: inv_freq must be a float64 vector on cuda:%d" % device)
+        rot, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    h, qs = 0, None
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
+            raise ValueError("kv_append: q must be [tokens, heads, head_dim]")
+        h, qs = q.shape[1], _heads(name, "q", q, dtype, device)
+    if q_out is not None and (q is None or q_out.shape != q.shape):
+        raise ValueError("kv_append: q_out must match q")
+
+    def run(handle):
+        out = torch.empty_like(q) if q is not None and q_out is None else q_out
+        qo = None if out is None else _heads(name, "q_out", out, dtype, device)
+        st = _lib().softmax_kv_append(cache, ks, vs, qs, qo, h, pos, ids, n, freq, rot,
+                                      1 if interleaved else 0, code, handle)
+        if st != OK:
+            raise SoftmaxError(st, name)
+        return out
+
+    return _on(device, stream, run)
 
 
 def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | None = None,
@@ -205,32 +205,34 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
     if q.dim() != 3:
         raise ValueError("attention_decode: q must be [sequences, heads, head_dim]")
     b, h, d = q.shape
-    code = _check(name, q, q=q, k_cache=k_cache, v_cache=v_cache)
-    device = q.device
-    cache = _cache(name, k_cache, v_cache, page_table, b)
-    hk = cache.n_kv_heads
-    if cache.head_dim != d or hk == 0 or h == 0 or h % hk:
+    device, code = _device_of(name, q)
+    dtype = q.dtype
+    cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
+    _, size, hk, dim = k_cache.shape
+    if dim != d or hk == 0 or h == 0 or h % hk:
         raise ValueError("attention_decode: the cache's heads do not match q")
-    lens = _index(name, "lengths", lengths, (b,), device)
-    if out is not None:
-        _check(name, q, out=out)
-        if out.shape != q.shape:
-            raise ValueError("attention_decode: out must match q")
-    with _on(device, stream) as handle:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        lse = torch.empty((b, h), dtype=torch.float32, device=device) if return_lse else None
+    if page_table.shape[0] != b:
+        raise ValueError("attention_decode: page_table must have a row for each query")
+    qs = _heads(name, "q", q, dtype, device)
+    lens = _index(name, "lengths", lengths, b, device)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("attention_decode: out must match q")
+
+    def run(handle):
+        o = torch.empty_like(q) if out is None else out
+        os = _heads(name, "out", o, dtype, device)
+        lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
         L = _lib()
-        need = L.softmax_attention_decode_workspace(b, h, hk, d,
-                                                    cache.table_width * cache.page_size)
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
-        st = L.softmax_attention_decode(cache, _heads(q), _heads(out),
-                                        lse.data_ptr() if return_lse else None, h, lens,
-                                        d ** -0.5 if scale is None else scale, code,
+        need = L.softmax_attention_decode_workspace(b, h, hk, d, page_table.shape[1] * size)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        st = L.softmax_attention_decode(cache, qs, os, lse.data_ptr() if return_lse else None, h,
+                                        lens, d ** -0.5 if scale is None else scale, code,
                                         ws.data_ptr() if need > 0 else None, max(need, 0), handle)
-    if st != OK:
-        raise SoftmaxError(st, name)
-    return (out, lse) if return_lse else out
+        if st != OK:
+            raise SoftmaxError(st, name)
+        return (o, lse) if return_lse else o
+
+    return _on(device, stream, run)
 
 
 def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causal: bool = True,
@@ -254,28 +256,31 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
         raise ValueError("attention_packed: q must be [total_q, heads, head_dim], k and v "
                          "[total_k, kv_heads, head_dim]")
     n, h, d = q.shape
-    m, hk = k.shape[0], k.shape[1]
+    m, hk, _ = k.shape
     if h == 0 or hk == 0 or h % hk:
         raise ValueError("attention_packed: heads must be a multiple of kv_heads")
-    code = _check(name, q, q=q, k=k, v=v)
-    device = q.device
-    if cu_q.dim() != 1 or cu_q.numel() < 1:
-        raise ValueError("attention_packed: cu_q must be a vector of sequences + 1 bounds")
+    device, code = _device_of(name, q)
+    dtype = q.dtype
+    qs, ks, vs = (_heads(name, "q", q, dtype, device), _heads(name, "k", k, dtype, device),
+                  _heads(name, "v", v, dtype, device))
     seqs = cu_q.numel() - 1
-    cq = _index(name, "cu_q", cu_q, (seqs + 1,), device)
-    ck = cq if cu_k is None else _index(name, "cu_k", cu_k, (seqs + 1,), device)
-    if out is not None:
-        _check(name, q, out=out)
-        if out.shape != q.shape:
-            raise ValueError("attention_packed: out must match q")
-    with _on(device, stream) as handle:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        lse = torch.empty((n, h), dtype=torch.float32, device=device) if return_lse else None
-        st = _lib().softmax_attention_packed(_heads(q), _heads(k), _heads(v), _heads(out),
-                                            lse.data_ptr() if return_lse else None, cq, ck, seqs,
-                                            n, m, h, hk, d, d ** -0.5 if scale is None else scale,
-                                            1 if causal else 0, code, handle)
-    if st != OK:
-        raise SoftmaxError(st, name)
-    return (out, lse) if return_lse else out
+    if seqs < 0:
+        raise ValueError("attention_packed: cu_q must be a vector of sequences + 1 bounds")
+    cq = _index(name, "cu_q", cu_q, seqs + 1, device)
+    ck = cq if cu_k is None else _index(name, "cu_k", cu_k, seqs + 1, device)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("attention_packed: out must match q")
+
+    def run(handle):
+        o = torch.empty_like(q) if out is None else out
+        os = _heads(name, "out", o, dtype, device)
+        lse = torch.empty((n, h), dtype=torch.float32, device=q.device) if return_lse else None
+        st = _lib().softmax_attention_packed(qs, ks, vs, os,
+                                             lse.data_ptr() if return_lse else None, cq, ck, seqs,
+                                             n, m, h, hk, d, d ** -0.5 if scale is None else scale,
+                                             1 if causal else 0, code, handle)
+        if st != OK:
+            raise SoftmaxError(st, name)
+        return (o, lse) if return_lse else o
+
+    return _on(device, stream, run)
