@@ -12,6 +12,9 @@
 //            workspace, two slots to a CTA (a run has at most one part at
 //            either end), and the join kernel merges an item's parts in token
 //            order, so results do not depend on timing.
+//            Short calls (a few tiles to a CTA) take a cluster of CTAs to an
+//            item instead and join through distributed shared memory: one
+//            launch and no workspace.
 //   warp     16 tokens of each tile, on its own: its K and V rows arrive by
 //            cp.async in its own ring of stages (no CTA barrier in the walk),
 //            rows past the length as zeros.  S = Q K^T by mma.sync m16n8k16
@@ -54,10 +57,17 @@ struct Begun {
     int64_t last;
 };
 
+// How a call is launched.  cluster > 0: a cluster of that many CTAs to an item
+// (CTA r takes tiles r, r + cluster, ...), joined through distributed shared
+// memory; one launch, no workspace.  cluster == 0: equal runs of all tiles
+// over a grid that fills the device, joined by a second kernel.
 struct DecodeShape {
     int32_t group, blocks;                          // heads per kv head, 16-head blocks of them
-    int32_t grid;
+    int32_t grid, cluster;
 };
+
+constexpr int kMaxCluster = 16;
+constexpr int kClusterTiles = 8;                    // tiles per CTA up to which clusters are used
 
 inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, int64_t capacity,
                                 int sm_count)
@@ -65,9 +75,20 @@ inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, i
     DecodeShape s;
     s.group = static_cast<int32_t>(n_heads / n_kv);
     s.blocks = (s.group + kRows - 1) / kRows;
-    const int64_t per = (capacity + kTile - 1) / kTile;
+    const int64_t per = (capacity + kTile - 1) / kTile > 0 ? (capacity + kTile - 1) / kTile : 1;
     const int64_t most = static_cast<int64_t>(sm_count) * kCtasPerSm;
     const int64_t items = n_seqs * n_kv * s.blocks;
+    s.cluster = 0;
+    if (items <= most) {
+        int c = 1;
+        while (c < kMaxCluster && c < per && items * c * 2 <= most)
+            c *= 2;
+        if (per <= static_cast<int64_t>(c) * kClusterTiles) {
+            s.cluster = c;
+            s.grid = static_cast<int32_t>(items * c);
+            return s;
+        }
+    }
     s.grid = static_cast<int32_t>(items >= most || items * per >= most ? most : items * per);
     return s;
 }
@@ -160,7 +181,7 @@ __device__ Run find_run(const DecodeProblem& p, int inner, int64_t* scratch)
     return r;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale_log2)
 {
@@ -181,26 +202,52 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
 
     pdl_launch_dependents();
     pdl_wait();
-    const Run run = find_run(p, inner, sm_scratch);
+    // The CTA's pieces: runs of tiles of items.  Cluster form: one piece, its
+    // tiles every `step`; run form: consecutive tiles, several items in turn.
+    const int step = CLUSTER ? sh.cluster : 1;
+    const int crank = CLUSTER ? static_cast<int>(blockIdx.x % static_cast<unsigned>(sh.cluster)) : 0;
+    Run run = {};
+    if constexpr (CLUSTER) {
+        run.end = 1;
+    } else {
+        run = find_run(p, inner, sm_scratch);
+    }
     int64_t seq = run.seq, before = run.before;
     int64_t begun_item = -1, begun_last = 0;
 
     const int r_a = lane >> 2, c_q = (lane & 3) * 2;
     for (int64_t at = run.begin; at < run.end;) {
-        // ---- the piece: tiles [t0, t1) of item (seq, in)
+        // ---- the piece: tiles t0, t0 + step, ... below t1 of item (seq, in)
         bool bad_len;
-        int32_t len = length_of(p, seq, bad_len);
-        int64_t nt = tiles_of(len);
-        while (at >= before + nt * inner) {         // next sequence
-            before += nt * inner;
-            ++seq;
+        int32_t len;
+        int in;
+        int64_t nt, first = 0, t0, t1;
+        int32_t page0 = -1;                         // cluster form: the first tile's page
+        if constexpr (CLUSTER) {
+            const int64_t item = blockIdx.x / static_cast<unsigned>(sh.cluster);
+            seq = item / inner;
+            in = static_cast<int>(item - seq * inner);
+            const int32_t tok = crank * kTile + warp * kWarpTokens + (lane & 15);
+            if (tok < p.cache.capacity)             // in flight beside the length
+                page0 = __ldg(p.cache.table + seq * p.cache.table_stride + divide(tok, p.cache.page));
             len = length_of(p, seq, bad_len);
             nt = tiles_of(len);
+            t0 = crank;
+            t1 = nt;
+        } else {
+            len = length_of(p, seq, bad_len);
+            nt = tiles_of(len);
+            while (at >= before + nt * inner) {     // next sequence
+                before += nt * inner;
+                ++seq;
+                len = length_of(p, seq, bad_len);
+                nt = tiles_of(len);
+            }
+            in = static_cast<int>((at - before) / nt);
+            first = before + in * nt;               // the item's first tile among all
+            t0 = at - first;
+            t1 = run.end - first < nt ? run.end - first : nt;
         }
-        const int in = static_cast<int>((at - before) / nt);
-        const int64_t first = before + in * nt;     // the item's first tile among all
-        const int64_t t0 = at - first;
-        const int64_t t1 = run.end - first < nt ? run.end - first : nt;
         const int kvh = in / sh.blocks, hb = in - kvh * sh.blocks;
         const int h0 = kvh * sh.group + hb * kRows;
         const int rows = sh.group - hb * kRows < kRows ? sh.group - hb * kRows : kRows;
@@ -225,16 +272,18 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
             static_cast<const unsigned short*>(p.cache.v) + kvh * p.cache.v_head;
         const int32_t* table = p.cache.table + seq * p.cache.table_stride;
 
-        // Copy this warp's block of tile t into its ring: lanes 0..15 look up
-        // their token's K row, lanes 16..31 its V row.
+        // Copy this warp's block of tile t into stage `st` of its ring: lanes
+        // 0..15 look up their token's K row, lanes 16..31 its V row.
         bool bad = bad_len;
-        auto issue = [&](int64_t t) {
-            const uint32_t dst = ring + static_cast<uint32_t>((t - t0) % kStages) * (2 * BLK);
+        if (CLUSTER && bad_len && crank == 0 && tid == 0)
+            atomicOr(&g_error_attention_decode, kErrBadIndex);
+        auto issue = [&](int64_t t, int st) {
+            const uint32_t dst = ring + static_cast<uint32_t>(st) * (2 * BLK);
             const int32_t tok = static_cast<int32_t>(t * kTile) + warp * kWarpTokens + (lane & 15);
             int64_t off = -1;
             if (tok < len) {
                 const uint32_t slot = divide(tok, p.cache.page);
-                const int32_t page = __ldg(table + slot);
+                const int32_t page = CLUSTER && t == t0 ? page0 : __ldg(table + slot);
                 if (page >= 0 && page < p.cache.n_pages) {
                     const int64_t row = tok - slot * p.cache.page.d;
                     off = lane < 16 ? page * p.cache.k_page + row * p.cache.k_row
@@ -261,17 +310,19 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
             acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
-            if (t0 + i < t1)
-                issue(t0 + i);
+            if (t0 + i * step < t1)
+                issue(t0 + i * step, i);
             cp_async_commit();
         }
-        for (int64_t t = t0; t < t1; ++t) {
-            if (t + kStages - 1 < t1)
-                issue(t + kStages - 1);
+        int now = 0;                                // the stage of tile t
+        for (int64_t t = t0; t < t1; t += step) {
+            if (t + (kStages - 1) * step < t1)
+                issue(t + (kStages - 1) * step, now == 0 ? kStages - 1 : now - 1);
             cp_async_commit();
             asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
             __syncwarp();
-            const uint32_t sK = ring + static_cast<uint32_t>((t - t0) % kStages) * (2 * BLK);
+            const uint32_t sK = ring + static_cast<uint32_t>(now) * (2 * BLK);
+            now = now + 1 == kStages ? 0 : now + 1;
             const uint32_t sV = sK + BLK;
             const int mi = lane >> 3;
 
@@ -370,11 +421,10 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
             *reinterpret_cast<float2*>(a + 8 * D) = make_float2(acc[i][2] * f_b, acc[i][3] * f_b);
         }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == nt;
-        Part<D>* const part = parts + 2 * static_cast<int64_t>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            float M = kNegInf, L = 0.0f;
+        // Row r, columns c .. c + 3 of the four warps' sum, with its (m, l).
+        auto sum_of = [&](int r, int c, float& M, float& L) {
+            M = kNegInf;
+            L = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 M = fmaxf(M, sm_m[w][r]);
@@ -386,16 +436,80 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
                 const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * kRows + r) * D + c);
                 o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
             }
+            return o;
+        };
+        auto store = [&](int r, int c, const float4& o, float M, float L) {
+            const float inv = 1.0f / L;
+            uint2 w2;
+            w2.x = Elem<T>::pack2(o.x * inv, o.y * inv);
+            w2.y = Elem<T>::pack2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.o.data) + seq * p.o.row +
+                                      static_cast<int64_t>(h0 + r) * p.o.head + c) = w2;
+            if (p.lse && c == 0)
+                p.lse[seq * p.n_heads + h0 + r] =
+                    L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+        };
+        if constexpr (CLUSTER) {
+            // Each CTA leaves its sum in the place of warp 0's; then CTA r
+            // merges every cluster-th group of four columns of all of them, in
+            // the order of the CTAs.
+            namespace cg = cooperative_groups;
+            if (sh.cluster > 1) {
+                float M[kRows * D / 4 / kThreads], L[kRows * D / 4 / kThreads];
+                float4 o[kRows * D / 4 / kThreads];
+#pragma unroll
+                for (int j = 0; j < kRows * D / 4 / kThreads; ++j) {
+                    const int i = tid + j * kThreads;
+                    o[j] = sum_of(i / (D / 4), (i % (D / 4)) * 4, M[j], L[j]);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kRows * D / 4 / kThreads; ++j) {
+                    const int i = tid + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+                    *reinterpret_cast<float4*>(sm_o + r * D + c) = o[j];
+                    if (c == 0) {
+                        sm_m[0][r] = M[j];
+                        sm_l[0][r] = L[j];
+                    }
+                }
+                cg::cluster_group cluster = cg::this_cluster();
+                cluster.sync();
+                for (int i = crank + tid * sh.cluster; i < rows * (D / 4);
+                     i += kThreads * sh.cluster) {
+                    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+                    float Mx = kNegInf, Lx = 0.0f;
+                    for (int q = 0; q < sh.cluster; ++q)
+                        Mx = fmaxf(Mx, *cluster.map_shared_rank(&sm_m[0][r], q));
+                    const float ref = Mx == kNegInf ? 0.0f : Mx;
+                    float4 acc4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int q = 0; q < sh.cluster; ++q) {
+                        const float f = ex2_ftz(*cluster.map_shared_rank(&sm_m[0][r], q) - ref);
+                        const float4 x = *reinterpret_cast<const float4*>(
+                            cluster.map_shared_rank(sm_o + r * D + c, q));
+                        Lx += *cluster.map_shared_rank(&sm_l[0][r], q) * f;
+                        acc4.x += x.x * f; acc4.y += x.y * f; acc4.z += x.z * f; acc4.w += x.w * f;
+                    }
+                    store(r, c, acc4, Mx, Lx);
+                }
+                cluster.sync();                     // read before a CTA leaves
+            } else {
+                for (int i = tid; i < rows * (D / 4); i += kThreads) {
+                    float M, L;
+                    const float4 o = sum_of(i / (D / 4), (i % (D / 4)) * 4, M, L);
+                    store(i / (D / 4), (i % (D / 4)) * 4, o, M, L);
+                }
+            }
+            return;
+        }
+        const bool whole = t0 == 0 && t1 == nt;
+        Part<D>* const part = parts + 2 * static_cast<int64_t>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float M, L;
+            const float4 o = sum_of(r, c, M, L);
             if (whole) {
-                const float inv = 1.0f / L;
-                uint2 w2;
-                w2.x = Elem<T>::pack2(o.x * inv, o.y * inv);
-                w2.y = Elem<T>::pack2(o.z * inv, o.w * inv);
-                *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.o.data) + seq * p.o.row +
-                                          static_cast<int64_t>(h0 + r) * p.o.head + c) = w2;
-                if (p.lse && c == 0)
-                    p.lse[seq * p.n_heads + h0 + r] =
-                        L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+                store(r, c, o, M, L);
             } else {
                 *reinterpret_cast<float4*>(part->o + r * D + c) = o;
                 if (c == 0) {
@@ -492,23 +606,26 @@ attention_decode_join_kernel(const DecodeProblem p, const DecodeShape sh)
 template <typename T, int D>
 cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
 {
-    auto* kern = attention_decode_kernel<T, D>;
+    const DecodeShape sh = decode_shape(p.n_seqs, p.n_heads, p.cache.n_kv_heads, p.cache.capacity,
+                                        sm_count_current());
+    auto* kern = sh.cluster > 0 ? attention_decode_kernel<T, D, true>
+                                : attention_decode_kernel<T, D, false>;
     const int smem = kWarps * kStages * 2 * kWarpTokens * D * 2;
     static_assert(kWarps * kRows * D * 4 <= kWarps * kStages * 2 * kWarpTokens * D * 2,
                   "the warps' O rows fit in the rings");
-    static std::atomic<bool> attr_set[64];
+    static std::atomic<bool> attr_set[2][64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return cudaErrorInvalidDevice;
-    if (!attr_set[dev].load()) {
-        const cudaError_t e =
+    if (!attr_set[sh.cluster > 0][dev].load()) {
+        cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && sh.cluster > 0)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
-        attr_set[dev].store(true);
+        attr_set[sh.cluster > 0][dev].store(true);
     }
-    const DecodeShape sh = decode_shape(p.n_seqs, p.n_heads, p.cache.n_kv_heads, p.cache.capacity,
-                                        sm_count_current());
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sh.grid), 1, 1);
@@ -516,11 +633,11 @@ cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, 1));
+    cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, sh.cluster));
     const float scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
     cudaError_t err = cudaLaunchKernelEx(&cfg, kern, p, sh, scale_log2);
     note_launch();
-    if (err != cudaSuccess)
+    if (err != cudaSuccess || sh.cluster > 0)
         return err;
     cfg.blockDim = dim3(kRows * 32, 1, 1);
     cfg.dynamicSmemBytes = 0;
@@ -535,6 +652,8 @@ size_t attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int64_t n_kv_
                                   int64_t head_dim, int64_t capacity)
 {
     const DecodeShape sh = decode_shape(n_seqs, n_heads, n_kv_heads, capacity, sm_count_current());
+    if (sh.cluster > 0)
+        return 0;
     const size_t part = head_dim == 64 ? sizeof(Part<64>) : sizeof(Part<128>);
     return static_cast<size_t>(sh.grid) * (2 * part + sizeof(Begun));
 }
