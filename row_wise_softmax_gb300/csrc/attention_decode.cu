@@ -3,7 +3,8 @@
 // running (m, l) softmax of "Triton GPU programming deep dive", section 3.3.
 //
 //   item     one (sequence, key/value head, block of up to 16 query heads of
-//            its group); its tokens are cut into tiles of 64.
+//            its group); its tokens are cut into tiles of 64
+//            (128 at D = 64).
 //   split    all tiles of all items, in order, are cut into as many equal
 //            runs as there are CTAs: a CTA's run may begin and end inside an
 //            item.  Lengths are on the device, so each CTA finds its run from
@@ -15,7 +16,7 @@
 //            Short calls (a few tiles to a CTA) take a cluster of CTAs to an
 //            item instead and join through distributed shared memory: one
 //            launch and no workspace.
-//   warp     16 tokens of each tile, on its own: its K and V rows arrive by
+//   warp     16 tokens (32 at D = 64) of each tile, on its own: its K and V rows arrive by
 //            cp.async in its own ring of stages (no CTA barrier in the walk),
 //            rows past the length as zeros.  S = Q K^T by mma.sync m16n8k16
 //            with the group's heads as the 16 rows; the scores' accumulator
@@ -38,10 +39,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                          // query heads of an item
-constexpr int kWarpTokens = 16;
-constexpr int kTile = kWarps * kWarpTokens;        // tokens of a tile
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
+constexpr float kLazyRescaleLog2 = 8.0f;           // weights <= 2^8 between rescales
+
+// Tokens of a tile and of a warp's block of it: a block of K and V is 8 KB at
+// either head dimension (16-token blocks at D = 64 spent half of the issue
+// slots on bookkeeping: 200 x 1000 tokens of 16 heads 150 us).
+__host__ __device__ constexpr int warp_tokens(int d) { return d == 128 ? 16 : 32; }
+__host__ __device__ constexpr int tile_tokens(int d) { return kWarps * warp_tokens(d); }
 
 // One part of an item in the workspace.
 template <int D>
@@ -67,15 +73,16 @@ struct DecodeShape {
 };
 
 constexpr int kMaxCluster = 16;
-constexpr int kClusterTiles = 8;                    // tiles per CTA up to which clusters are used
+constexpr int kClusterTiles = 16;                   // tiles per CTA up to which clusters are used
 
-inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, int64_t capacity,
-                                int sm_count)
+inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, int64_t head_dim,
+                                int64_t capacity, int sm_count)
 {
     DecodeShape s;
     s.group = static_cast<int32_t>(n_heads / n_kv);
     s.blocks = (s.group + kRows - 1) / kRows;
-    const int64_t per = (capacity + kTile - 1) / kTile > 0 ? (capacity + kTile - 1) / kTile : 1;
+    const int tile = tile_tokens(static_cast<int>(head_dim));
+    const int64_t per = capacity > 0 ? (capacity + tile - 1) / tile : 1;
     const int64_t most = static_cast<int64_t>(sm_count) * kCtasPerSm;
     const int64_t items = n_seqs * n_kv * s.blocks;
     s.cluster = 0;
@@ -111,13 +118,412 @@ __device__ __forceinline__ int32_t length_of(const DecodeProblem& p, int64_t b, 
 
 // Tiles of an item of n tokens: at least one, so that an empty sequence's
 // outputs are written too.
-__device__ __forceinline__ int64_t tiles_of(int32_t n)
+template <int D>
+__device__ __forceinline__ int32_t tiles_of(int32_t n)
 {
-    return n == 0 ? 1 : (n + kTile - 1) / kTile;
+    constexpr int tile = tile_tokens(D);
+    return n == 0 ? 1 : (n + tile - 1) / tile;
 }
 
-// The CTA's run [begin, end) of all tiles, and the item it begins in.  Every
-// thread gets the same answer.
+// What a warp carries through an item: the running maxima (base 2), sums and
+// output accumulators of rows lane / 4 and lane / 4 + 8, in the accumulator
+// layout of m16n8k16 (columns (lane % 4) * 2, + 1 of each 8).
+template <int D>
+struct WarpSum {
+    float m_a, m_b, l_a, l_b;
+    float acc[D / 8][4];
+
+    __device__ __forceinline__ void clear()
+    {
+        m_a = m_b = kNegInf;
+        l_a = l_b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    }
+
+    // The row sums over the four lanes that share a row; NaN for an item with
+    // a bad page or length.
+    __device__ __forceinline__ void close(bool bad)
+    {
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+        if (__any_sync(0xffffffffu, bad)) {
+            l_a = l_b = __int_as_float(0x7fc00000);
+            if ((threadIdx.x & 31) == 0)
+                atomicOr(&g_error_attention_decode, kErrBadIndex);
+        }
+    }
+};
+
+// Q fragments (A operand) of `rows` heads from h0 on; rows past them are zero.
+template <int D>
+__device__ __forceinline__ void load_q(const DecodeProblem& p, int64_t seq, int h0, int rows,
+                                       uint32_t (&qa)[D / 16][4])
+{
+    const int lane = threadIdx.x & 31, r_a = lane >> 2, c_q = (lane & 3) * 2;
+    const unsigned short* gq = static_cast<const unsigned short*>(p.q.data) + seq * p.q.row +
+                               static_cast<int64_t>(h0) * p.q.head;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = r_a + (e & 1) * 8, c = kk * 16 + (e >> 1) * 8 + c_q;
+            qa[kk][e] = r < rows ? __ldg(reinterpret_cast<const unsigned*>(gq + r * p.q.head + c))
+                                 : 0u;
+        }
+}
+
+// The page that holds token `tok`, -1 past the length.
+__device__ __forceinline__ int32_t page_of(const DecodeProblem& p, const int32_t* table,
+                                           int32_t tok, int32_t len)
+{
+    return tok < len ? __ldg(table + divide(tok, p.cache.page)) : -1;
+}
+
+// Copy a warp's block of K and V rows of one head into a stage: lane i holds
+// the page of token tok0 + i (of 16 tokens, lanes 16..31 hold them again) and
+// turns it into its rows' places, in units of 16 bytes.  Tokens past the
+// length, and rows of bad pages (true is returned then), arrive as zeros.
+template <int D>
+__device__ __forceinline__ bool copy_block(const DecodeProblem& p, int kvh, int32_t tok0,
+                                           int32_t page, int32_t len, uint32_t dst)
+{
+    constexpr int TOK = warp_tokens(D);
+    constexpr int CH = D / 8;                       // 16-byte chunks of a row
+    constexpr uint32_t BLK = TOK * D * 2;
+    const int lane = threadIdx.x & 31;
+    const unsigned short* gk =
+        static_cast<const unsigned short*>(p.cache.k) + kvh * p.cache.k_head;
+    const unsigned short* gv =
+        static_cast<const unsigned short*>(p.cache.v) + kvh * p.cache.v_head;
+    const int32_t tok = tok0 + lane % TOK;
+    const bool held = page >= 0 && page < p.cache.n_pages && tok < len;
+    int64_t ko = -1, vo = -1;
+    if (held) {
+        const int64_t row = tok - divide(tok, p.cache.page) * p.cache.page.d;
+        ko = (page * p.cache.k_page + row * p.cache.k_row) >> 3;
+        vo = (page * p.cache.v_page + row * p.cache.v_row) >> 3;
+    }
+    auto copy = [&](int i, int64_t k, int64_t v) {
+        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+        const int bytes = k < 0 ? 0 : 16;
+        k = k < 0 ? 0 : k * 8 + c * 8;
+        v = v < 0 ? 0 : v * 8 + c * 8;
+        cp_async16_zfill(dst + tile_off<D>(r, c), gk + k, bytes);
+        cp_async16_zfill(dst + BLK + tile_off<D>(r, c), gv + v, bytes);
+    };
+    if (p.cache.near_rows) {                        // places below 2^31, the same for K and V
+#pragma unroll
+        for (int i = 0; i < TOK * CH / 32; ++i) {
+            const int32_t o = __shfl_sync(0xffffffffu, static_cast<int32_t>(ko), (i * 32 + lane) / CH);
+            copy(i, o, o);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < TOK * CH / 32; ++i) {
+            const int r = (i * 32 + lane) / CH;
+            copy(i, shfl64(ko, r), shfl64(vo, r));
+        }
+    }
+    return tok < len && !held;
+}
+
+// A warp's block of tokens, the first at position j0, of a sequence of len:
+// S = Q K^T, the softmax's step, O += P V.  The reference of the softmax moves
+// only when a maximum exceeds it by more than 2^8; l and O agree either way.
+template <typename T, int D>
+__device__ __forceinline__ void attend_block(const uint32_t (&qa)[D / 16][4], uint32_t sK,
+                                             int32_t j0, int32_t len, float scale_log2,
+                                             WarpSum<D>& w)
+{
+    constexpr int TOK = warp_tokens(D);
+    constexpr int NB = TOK / 8;
+    const uint32_t sV = sK + TOK * D * 2;
+    const int lane = threadIdx.x & 31, mi = lane >> 3, c_q = (lane & 3) * 2;
+    float s[NB][4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int n = 0; n < NB; n += 2) {
+            uint32_t bk[4];
+            ldsm_x4(bk, sK + tile_off<D>(n * 8 + (lane & 7) + (mi >> 1) * 8, kk * 2 + (mi & 1)));
+            MmaType<T>::mma(s[n], qa[kk], bk[0], bk[1]);
+            MmaType<T>::mma(s[n + 1], qa[kk], bk[2], bk[3]);
+        }
+    if (j0 + TOK > len) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (j0 + n * 8 + c_q + e >= len)
+                    s[n][e] = s[n][2 + e] = kNegInf;
+    }
+    float mx_a = kNegInf, mx_b = kNegInf;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        mx_a = max3(mx_a, s[n][0], s[n][1]);
+        mx_b = max3(mx_b, s[n][2], s[n][3]);
+    }
+    mx_a *= scale_log2;
+    mx_b *= scale_log2;
+    // Rows are shared by four lanes, whose maxima are exchanged only when one
+    // of them passes the reference.
+    if (__any_sync(0xffffffffu,
+                   mx_a > w.m_a + kLazyRescaleLog2 || mx_b > w.m_b + kLazyRescaleLog2)) {
+        mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
+        mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
+        const float mn_a = fmaxf(w.m_a, mx_a), mn_b = fmaxf(w.m_b, mx_b);
+        const float al_a = mn_a == kNegInf ? 1.0f : ex2_ftz(w.m_a - mn_a);
+        const float al_b = mn_b == kNegInf ? 1.0f : ex2_ftz(w.m_b - mn_b);
+        w.m_a = mn_a;
+        w.m_b = mn_b;
+        w.l_a *= al_a;
+        w.l_b *= al_b;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            w.acc[i][0] *= al_a; w.acc[i][1] *= al_a;
+            w.acc[i][2] *= al_b; w.acc[i][3] *= al_b;
+        }
+    }
+    const float ref_a = w.m_a == kNegInf ? 0.0f : -w.m_a;
+    const float ref_b = w.m_b == kNegInf ? 0.0f : -w.m_b;
+    uint32_t pa[TOK / 16][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const float p0 = ex2_ftz(fmaf(s[n][0], scale_log2, ref_a));
+        const float p1 = ex2_ftz(fmaf(s[n][1], scale_log2, ref_a));
+        const float p2 = ex2_ftz(fmaf(s[n][2], scale_log2, ref_b));
+        const float p3 = ex2_ftz(fmaf(s[n][3], scale_log2, ref_b));
+        w.l_a += p0 + p1;
+        w.l_b += p2 + p3;
+        pa[n / 2][(n % 2) * 2 + 0] = Elem<T>::pack2(p0, p1);
+        pa[n / 2][(n % 2) * 2 + 1] = Elem<T>::pack2(p2, p3);
+    }
+#pragma unroll
+    for (int k = 0; k < TOK / 16; ++k)
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+            uint32_t bv[4];
+            ldsm_x4_trans(bv, sV + tile_off<D>(k * 16 + (lane & 7) + (mi & 1) * 8,
+                                               dp * 2 + (mi >> 1)));
+            MmaType<T>::mma(w.acc[2 * dp], pa[k], bv[0], bv[1]);
+            MmaType<T>::mma(w.acc[2 * dp + 1], pa[k], bv[2], bv[3]);
+        }
+}
+
+// Columns c .. c + 3 of head h's output from its sum and (m, l); the logsumexp.
+template <typename T>
+__device__ __forceinline__ void store_head(const DecodeProblem& p, int64_t seq, int h, int c,
+                                           const float4& o, float M, float L)
+{
+    const float inv = 1.0f / L;
+    uint2 w;
+    w.x = Elem<T>::pack2(o.x * inv, o.y * inv);
+    w.y = Elem<T>::pack2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.o.data) + seq * p.o.row +
+                              static_cast<int64_t>(h) * p.o.head + c) = w;
+    if (p.lse && c == 0)
+        p.lse[seq * p.n_heads + h] = L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+// The (m, l) of every warp's rows, and row r's over the warps.
+struct RowStats {
+    float m[kWarps][kRows], l[kWarps][kRows];
+
+    template <int D>
+    __device__ __forceinline__ void put(const WarpSum<D>& w)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if ((lane & 3) == 0) {
+            m[warp][lane >> 2] = w.m_a;
+            m[warp][(lane >> 2) + 8] = w.m_b;
+            l[warp][lane >> 2] = w.l_a;
+            l[warp][(lane >> 2) + 8] = w.l_b;
+        }
+    }
+
+    __device__ __forceinline__ float max_of(int r) const
+    {
+        float M = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            M = fmaxf(M, m[w][r]);
+        return M;
+    }
+
+    __device__ __forceinline__ float sum_of(int r, float M) const
+    {
+        const float ref = M == kNegInf ? 0.0f : M;
+        float L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            L += l[w][r] * ex2_ftz(m[w][r] - ref);
+        return L;
+    }
+
+    // What this warp's row r counts for in the merged sum.
+    __device__ __forceinline__ float factor(float mine, float M) const
+    {
+        return M == kNegInf ? 0.0f : ex2_ftz(mine - M);
+    }
+};
+
+// Which heads an item is: `in` counts (kv head, block of 16 query heads).
+struct ItemHeads {
+    int kvh, h0, rows;
+
+    __device__ __forceinline__ ItemHeads(const DecodeShape& sh, int in)
+    {
+        kvh = in / sh.blocks;
+        const int hb = in - kvh * sh.blocks;
+        h0 = kvh * sh.group + hb * kRows;
+        rows = sh.group - hb * kRows < kRows ? sh.group - hb * kRows : kRows;
+    }
+};
+
+// ------------------------------------------------- a cluster of CTAs per item
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+attention_decode_cluster_kernel(const DecodeProblem p, const DecodeShape sh, float scale_log2)
+{
+    namespace cg = cooperative_groups;
+    constexpr int TOK = warp_tokens(D), kTile = tile_tokens(D);
+    constexpr uint32_t BLK = TOK * D * 2;           // bytes of a warp's K (or V) block
+    constexpr int PER = kRows * D / 4 / kThreads;   // groups of four columns per thread
+    extern __shared__ __align__(128) unsigned char dec_smem[];
+    __shared__ RowStats stats;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t ring = smem_addr(dec_smem) + warp * (kStages * 2 * BLK);
+    float* const sm_o = reinterpret_cast<float*>(dec_smem);          // [kWarps][kRows][D]
+    const int step = sh.cluster;
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(step));
+    const int inner = p.cache.n_kv_heads * sh.blocks;
+    const int64_t item = blockIdx.x / static_cast<unsigned>(step);
+    const int64_t seq = item / inner;
+    const ItemHeads it(sh, static_cast<int>(item - seq * inner));
+
+    pdl_launch_dependents();
+    pdl_wait();
+    // The first tile's page, the length and Q are read side by side.
+    const int32_t* table = p.cache.table + seq * p.cache.table_stride;
+    const int32_t tok0 = warp * TOK + lane % TOK;
+    const int32_t page0 = page_of(p, table, rank * kTile + tok0, p.cache.capacity);
+    bool bad;
+    const int32_t len = length_of(p, seq, bad);
+    uint32_t qa[D / 16][4];
+    load_q<D>(p, seq, it.h0, it.rows, qa);
+    const int n_tiles = tiles_of<D>(len);
+
+    WarpSum<D> w;
+    w.clear();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        const int t = rank + i * step;
+        if (t < n_tiles)
+            bad |= copy_block<D>(p, it.kvh, t * kTile + warp * TOK,
+                                 i == 0 ? page0 : page_of(p, table, t * kTile + tok0, len), len,
+                                 ring + i * (2 * BLK));
+        cp_async_commit();
+    }
+    int now = 0;                                    // the stage of tile t
+    for (int t = rank; t < n_tiles; t += step) {
+        const int next = t + (kStages - 1) * step;
+        if (next < n_tiles)
+            bad |= copy_block<D>(p, it.kvh, next * kTile + warp * TOK,
+                                 page_of(p, table, next * kTile + tok0, len), len,
+                                 ring + (now == 0 ? kStages - 1 : now - 1) * (2 * BLK));
+        cp_async_commit();
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+        __syncwarp();
+        attend_block<T, D>(qa, ring + now * (2 * BLK), t * kTile + warp * TOK, len,
+                           scale_log2, w);
+        __syncwarp();                               // the stage may be refilled
+        now = now + 1 == kStages ? 0 : now + 1;
+    }
+    cp_async_wait_all_groups();
+
+    // ---- the four warps' sums into one
+    w.close(bad);
+    stats.put(w);
+    __syncthreads();                                // and every warp's ring is free
+    const int r_a = lane >> 2, c_q = (lane & 3) * 2;
+    const float f_a = stats.factor(w.m_a, stats.max_of(r_a));
+    const float f_b = stats.factor(w.m_b, stats.max_of(r_a + 8));
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+        float* const a = sm_o + (warp * kRows + r_a) * D + i * 8 + c_q;
+        *reinterpret_cast<float2*>(a) = make_float2(w.acc[i][0] * f_a, w.acc[i][1] * f_a);
+        *reinterpret_cast<float2*>(a + 8 * D) = make_float2(w.acc[i][2] * f_b, w.acc[i][3] * f_b);
+    }
+    __syncthreads();
+    float M[PER], L[PER];
+    float4 o[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+        M[j] = stats.max_of(r);
+        L[j] = stats.sum_of(r, M[j]);
+        o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(sm_o + (q * kRows + r) * D + c);
+            o[j].x += x.x; o[j].y += x.y; o[j].z += x.z; o[j].w += x.w;
+        }
+    }
+    if (step == 1) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = tid + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+            if (r < it.rows)
+                store_head<T>(p, seq, it.h0 + r, c, o[j], M[j], L[j]);
+        }
+        return;
+    }
+    // ---- each CTA leaves its sum in the place of warp 0's, and takes every
+    // cluster-th group of four columns of all of them, in the order of the CTAs
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+        *reinterpret_cast<float4*>(sm_o + r * D + c) = o[j];
+        if (c == 0) {
+            stats.m[0][r] = M[j];
+            stats.l[0][r] = L[j];
+        }
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int i = rank + tid * step; i < it.rows * (D / 4); i += kThreads * step) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        float Mx = kNegInf, Lx = 0.0f;
+#pragma unroll 8
+        for (int q = 0; q < step; ++q)
+            Mx = fmaxf(Mx, *cluster.map_shared_rank(&stats.m[0][r], q));
+        const float ref = Mx == kNegInf ? 0.0f : Mx;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int q = 0; q < step; ++q) {
+            const float f = ex2_ftz(*cluster.map_shared_rank(&stats.m[0][r], q) - ref);
+            const float4 x =
+                *reinterpret_cast<const float4*>(cluster.map_shared_rank(sm_o + r * D + c, q));
+            Lx += *cluster.map_shared_rank(&stats.l[0][r], q) * f;
+            sum.x += x.x * f; sum.y += x.y * f; sum.z += x.z * f; sum.w += x.w * f;
+        }
+        store_head<T>(p, seq, it.h0 + r, c, sum, Mx, Lx);
+    }
+    cluster.sync();                                 // read before a CTA leaves
+}
+
+// ------------------------------------------------------- equal runs of tiles
+// A CTA's run [begin, end) of all tiles, and the sequence it begins in.
 struct Run {
     int64_t begin, end;                             // tiles
     int64_t total, runs;
@@ -125,412 +531,249 @@ struct Run {
     int64_t before;                                 // tiles of the sequences before it
 };
 
-__device__ Run find_run(const DecodeProblem& p, int inner, int64_t* scratch)
+// Every thread gets the same answer.  The sequences' tiles are summed 128 at a
+// time; with no more sequences than that, one pass finds total and place.
+template <int D>
+__device__ Run find_run(const DecodeProblem& p, int inner, Run& place, int64_t* scratch)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0;
-    for (int64_t b = tid; b < p.n_seqs; b += kThreads) {
-        bool bad;
-        mine += tiles_of(length_of(p, b, bad));
+    auto scan = [&](int64_t b, int64_t& upto) {     // tiles of sequence b, and of the block up to it
+        bool bad = false;
+        const int64_t n = b < p.n_seqs ? tiles_of<D>(length_of(p, b, bad)) : 0;
         if (bad && blockIdx.x == 0)
             atomicOr(&g_error_attention_decode, kErrBadIndex);
+        upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += up;
+        }
+        __syncthreads();                            // scratch is free
+        if (lane == 31)
+            scratch[warp] = upto;
+        __syncthreads();
+        int64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp)
+                upto += scratch[w];
+            all += scratch[w];
+        }
+        return n;
+    };
+    auto all = [&] {
+        int64_t sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            sum += scratch[w];
+        return sum;
+    };
+    Run r = {};
+    int64_t upto, n = 0, total = 0;
+    for (int64_t b = 0; b < p.n_seqs; b += kThreads) {
+        n = scan(b + tid, upto);
+        total += all();
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0)
-        scratch[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        total += scratch[w];
-    total *= inner;
-    Run r;
     // No run is empty but those of the CTAs past the last tile: an item's
     // parts lie in consecutive CTAs.
-    r.total = total;
-    r.runs = total < gridDim.x ? total : gridDim.x;
-    r.begin = blockIdx.x < r.runs ? total * blockIdx.x / r.runs : 0;
-    r.end = blockIdx.x < r.runs ? total * (blockIdx.x + 1) / r.runs : 0;
-    r.seq = 0;
-    r.before = 0;
-    // Walk the sequences 32 at a time to the one that holds tile `begin`.
-    if (r.begin < r.end) {
-        for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
-            bool bad;
-            const int64_t n = b0 + lane < p.n_seqs
-                                  ? tiles_of(length_of(p, b0 + lane, bad)) * inner : 0;
-            int64_t sum = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o)
-                    sum += up;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, r.before + sum > r.begin);
-            if (past) {
-                const int at = __ffs(past) - 1;
-                r.before += shfl64(sum - n, at);
-                r.seq = b0 + at;
-                break;
-            }
-            r.before += shfl64(sum, 31);
+    r.total = total * inner;
+    r.runs = r.total < gridDim.x ? r.total : gridDim.x;
+    r.begin = blockIdx.x < r.runs ? r.total * blockIdx.x / r.runs : 0;
+    r.end = blockIdx.x < r.runs ? r.total * (blockIdx.x + 1) / r.runs : 0;
+    int64_t before = 0;
+    for (int64_t b = 0; b < p.n_seqs; b += kThreads) {
+        if (p.n_seqs > kThreads)
+            n = scan(b + tid, upto);
+        if (r.begin < r.end && n > 0 && (before + upto - n) * inner <= r.begin &&
+            r.begin < (before + upto) * inner) {
+            place.seq = b + tid;
+            place.before = (before + upto - n) * inner;
         }
+        before += all();
     }
+    __syncthreads();
+    r.seq = place.seq;
+    r.before = place.before;
     return r;
 }
 
-template <typename T, int D, bool CLUSTER>
+// A place in the order of all tiles: tile t of item (seq, in).
+template <int D>
+struct Cursor {
+    int64_t seq, first;                             // first: the item's first tile among all
+    int32_t in, t, n_tiles, len;
+    bool bad;                                       // the length is
+
+    __device__ __forceinline__ void read(const DecodeProblem& p)
+    {
+        len = length_of(p, seq, bad);
+        n_tiles = tiles_of<D>(len);
+    }
+
+    __device__ __forceinline__ void begin(const DecodeProblem& p, const Run& run)
+    {
+        seq = run.seq;
+        read(p);
+        const int64_t at = run.begin - run.before;
+        in = static_cast<int32_t>(at / n_tiles);
+        t = static_cast<int32_t>(at - static_cast<int64_t>(in) * n_tiles);
+        first = run.before + static_cast<int64_t>(in) * n_tiles;
+    }
+
+    // To the next item (there must be one).
+    __device__ __forceinline__ void next_item(const DecodeProblem& p, int inner)
+    {
+        first += n_tiles;
+        t = 0;
+        if (++in == inner) {
+            in = 0;
+            ++seq;
+            read(p);
+        }
+    }
+};
+
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale_log2)
+attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float scale_log2)
 {
-    constexpr int KS = D / 16;                      // k-steps over the head dimension
-    constexpr int DB = D / 8;                       // 8-wide output column blocks
-    constexpr int CH = D / 8;                       // 16-byte chunks of a row
-    constexpr uint32_t BLK = kWarpTokens * D * 2;   // bytes of a warp's K (or V) block
+    constexpr int TOK = warp_tokens(D), kTile = tile_tokens(D);
+    constexpr uint32_t BLK = TOK * D * 2;           // bytes of a warp's K (or V) block
     extern __shared__ __align__(128) unsigned char dec_smem[];
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+    __shared__ RowStats stats;
     __shared__ int64_t sm_scratch[kWarps];
+    __shared__ Run sm_place;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int inner = p.cache.n_kv_heads * sh.blocks;
     const uint32_t ring = smem_addr(dec_smem) + warp * (kStages * 2 * BLK);
-    float* const sm_o = reinterpret_cast<float*>(dec_smem);          // [kWarps][kRows][D]
+    // Eight rows of every warp's O: half an item at a time, beside the rings,
+    // which go on filling.
+    float* const sm_o = reinterpret_cast<float*>(dec_smem + kWarps * kStages * 2 * BLK);
     Part<D>* const parts = static_cast<Part<D>*>(p.workspace);
     Begun* const begun = reinterpret_cast<Begun*>(parts + 2 * static_cast<int64_t>(sh.grid));
 
     pdl_launch_dependents();
     pdl_wait();
-    // The CTA's pieces: runs of tiles of items.  Cluster form: one piece, its
-    // tiles every `step`; run form: consecutive tiles, several items in turn.
-    const int step = CLUSTER ? sh.cluster : 1;
-    const int crank = CLUSTER ? static_cast<int>(blockIdx.x % static_cast<unsigned>(sh.cluster)) : 0;
-    Run run = {};
-    if constexpr (CLUSTER) {
-        run.end = 1;
-    } else {
-        run = find_run(p, inner, sm_scratch);
-    }
-    int64_t seq = run.seq, before = run.before;
+    const Run run = find_run<D>(p, inner, sm_place, sm_scratch);
     int64_t begun_item = -1, begun_last = 0;
-
-    const int r_a = lane >> 2, c_q = (lane & 3) * 2;
-    for (int64_t at = run.begin; at < run.end;) {
-        // ---- the piece: tiles t0, t0 + step, ... below t1 of item (seq, in)
-        bool bad_len;
-        int32_t len;
-        int in;
-        int64_t nt, first = 0, t0, t1;
-        int32_t page0 = -1;                         // cluster form: the first tile's page
-        if constexpr (CLUSTER) {
-            const int64_t item = blockIdx.x / static_cast<unsigned>(sh.cluster);
-            seq = item / inner;
-            in = static_cast<int>(item - seq * inner);
-            const int32_t tok = crank * kTile + warp * kWarpTokens + (lane & 15);
-            if (tok < p.cache.capacity)             // in flight beside the length
-                page0 = __ldg(p.cache.table + seq * p.cache.table_stride + divide(tok, p.cache.page));
-            len = length_of(p, seq, bad_len);
-            nt = tiles_of(len);
-            t0 = crank;
-            t1 = nt;
-        } else {
-            len = length_of(p, seq, bad_len);
-            nt = tiles_of(len);
-            while (at >= before + nt * inner) {     // next sequence
-                before += nt * inner;
-                ++seq;
-                len = length_of(p, seq, bad_len);
-                nt = tiles_of(len);
+    if (run.begin < run.end) {
+        // Two cursors walk the run: one copies, kStages - 1 tiles ahead and on
+        // into the next items, the other computes.
+        Cursor<D> copy, it;
+        it.begin(p, run);
+        copy = it;
+        int64_t to_copy = run.end - run.begin;
+        uint32_t bad_stages = 0;
+        const int32_t tok0 = warp * TOK + lane % TOK;
+        auto copy_next = [&](int st) {
+            if (to_copy > 0) {
+                --to_copy;
+                const int32_t t = copy.t * kTile;
+                const bool bad = copy_block<D>(
+                    p, copy.in / sh.blocks, t + warp * TOK,
+                    page_of(p, p.cache.table + copy.seq * p.cache.table_stride, t + tok0, copy.len),
+                    copy.len, ring + static_cast<uint32_t>(st) * (2 * BLK));
+                bad_stages = (bad_stages & ~(1u << st)) | (bad ? 1u << st : 0u);
+                if (++copy.t == copy.n_tiles && to_copy > 0)
+                    copy.next_item(p, inner);
             }
-            in = static_cast<int>((at - before) / nt);
-            first = before + in * nt;               // the item's first tile among all
-            t0 = at - first;
-            t1 = run.end - first < nt ? run.end - first : nt;
-        }
-        const int kvh = in / sh.blocks, hb = in - kvh * sh.blocks;
-        const int h0 = kvh * sh.group + hb * kRows;
-        const int rows = sh.group - hb * kRows < kRows ? sh.group - hb * kRows : kRows;
-
-        // Q fragments (A operand): rows past the group are zero.
-        uint32_t qa[KS][4];
-        {
-            const unsigned short* gq = static_cast<const unsigned short*>(p.q.data) +
-                                       seq * p.q.row + static_cast<int64_t>(h0) * p.q.head;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = r_a + (e & 1) * 8, c = kk * 16 + (e >> 1) * 8 + c_q;
-                    qa[kk][e] = r < rows ? __ldg(reinterpret_cast<const unsigned*>(
-                                               gq + r * p.q.head + c)) : 0u;
-                }
-        }
-        const unsigned short* gk =
-            static_cast<const unsigned short*>(p.cache.k) + kvh * p.cache.k_head;
-        const unsigned short* gv =
-            static_cast<const unsigned short*>(p.cache.v) + kvh * p.cache.v_head;
-        const int32_t* table = p.cache.table + seq * p.cache.table_stride;
-
-        // Copy this warp's block of tile t into stage `st` of its ring: lanes
-        // 0..15 look up their token's K row, lanes 16..31 its V row.
-        bool bad = bad_len;
-        if (CLUSTER && bad_len && crank == 0 && tid == 0)
-            atomicOr(&g_error_attention_decode, kErrBadIndex);
-        auto issue = [&](int64_t t, int st) {
-            const uint32_t dst = ring + static_cast<uint32_t>(st) * (2 * BLK);
-            const int32_t tok = static_cast<int32_t>(t * kTile) + warp * kWarpTokens + (lane & 15);
-            int64_t off = -1;
-            if (tok < len) {
-                const uint32_t slot = divide(tok, p.cache.page);
-                const int32_t page = CLUSTER && t == t0 ? page0 : __ldg(table + slot);
-                if (page >= 0 && page < p.cache.n_pages) {
-                    const int64_t row = tok - slot * p.cache.page.d;
-                    off = lane < 16 ? page * p.cache.k_page + row * p.cache.k_row
-                                    : page * p.cache.v_page + row * p.cache.v_row;
-                } else {
-                    bad = true;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kWarpTokens * CH / 32; ++i) {
-                const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-                const int64_t ko = shfl64(off, r), vo = shfl64(off, r + 16);
-                cp_async16_zfill(dst + tile_off<D>(r, c), gk + (ko < 0 ? 0 : ko + c * 8),
-                                 ko < 0 ? 0 : 16);
-                cp_async16_zfill(dst + BLK + tile_off<D>(r, c), gv + (vo < 0 ? 0 : vo + c * 8),
-                                 vo < 0 ? 0 : 16);
-            }
+            cp_async_commit();
         };
-
-        float m_a = kNegInf, m_b = kNegInf, l_a = 0.0f, l_b = 0.0f;
-        float acc[DB][4];
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
-            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (t0 + i * step < t1)
-                issue(t0 + i * step, i);
-            cp_async_commit();
+        for (int i = 0; i < kStages - 1; ++i)
+            copy_next(i);
+        uint32_t qa[D / 16][4];
+        {
+            const ItemHeads heads(sh, it.in);
+            load_q<D>(p, it.seq, heads.h0, heads.rows, qa);
         }
-        int now = 0;                                // the stage of tile t
-        for (int64_t t = t0; t < t1; t += step) {
-            if (t + (kStages - 1) * step < t1)
-                issue(t + (kStages - 1) * step, now == 0 ? kStages - 1 : now - 1);
-            cp_async_commit();
+        WarpSum<D> w;
+        w.clear();
+        bool bad = it.bad;
+        int32_t from = it.t;                        // the piece's first tile
+        int now = 0;                                // the stage of the tile at hand
+        for (int64_t left = run.end - run.begin; left > 0; --left) {
+            copy_next(now == 0 ? kStages - 1 : now - 1);
             asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
             __syncwarp();
-            const uint32_t sK = ring + static_cast<uint32_t>(now) * (2 * BLK);
-            now = now + 1 == kStages ? 0 : now + 1;
-            const uint32_t sV = sK + BLK;
-            const int mi = lane >> 3;
-
-            float s[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                uint32_t bk[4];
-                ldsm_x4(bk, sK + tile_off<D>((lane & 7) + (mi >> 1) * 8, kk * 2 + (mi & 1)));
-                MmaType<T>::mma(s[0], qa[kk], bk[0], bk[1]);
-                MmaType<T>::mma(s[1], qa[kk], bk[2], bk[3]);
-            }
-            const int32_t j0 = static_cast<int32_t>(t * kTile) + warp * kWarpTokens;
-            float mx_a = kNegInf, mx_b = kNegInf;
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool past = j0 + nb * 8 + c_q + e >= len;
-                    const float xa = past ? kNegInf : s[nb][e] * scale_log2;
-                    const float xb = past ? kNegInf : s[nb][2 + e] * scale_log2;
-                    s[nb][e] = xa;
-                    s[nb][2 + e] = xb;
-                    mx_a = fmaxf(mx_a, xa);
-                    mx_b = fmaxf(mx_b, xb);
-                }
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
-            const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
-            const float ref_a = mn_a == kNegInf ? 0.0f : mn_a;
-            const float ref_b = mn_b == kNegInf ? 0.0f : mn_b;
-            const float al_a = ex2_ftz(m_a - ref_a), al_b = ex2_ftz(m_b - ref_b);
-            m_a = mn_a;
-            m_b = mn_b;
-            l_a *= al_a;
-            l_b *= al_b;
-#pragma unroll
-            for (int i = 0; i < DB; ++i) {
-                acc[i][0] *= al_a; acc[i][1] *= al_a;
-                acc[i][2] *= al_b; acc[i][3] *= al_b;
-            }
-            uint32_t pa[4];
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-                const float p0 = ex2_ftz(s[nb][0] - ref_a), p1 = ex2_ftz(s[nb][1] - ref_a);
-                const float p2 = ex2_ftz(s[nb][2] - ref_b), p3 = ex2_ftz(s[nb][3] - ref_b);
-                l_a += p0 + p1;
-                l_b += p2 + p3;
-                pa[nb * 2 + 0] = Elem<T>::pack2(p0, p1);
-                pa[nb * 2 + 1] = Elem<T>::pack2(p2, p3);
-            }
-#pragma unroll
-            for (int dp = 0; dp < D / 16; ++dp) {
-                uint32_t bv[4];
-                ldsm_x4_trans(bv, sV + tile_off<D>((lane & 7) + (mi & 1) * 8, dp * 2 + (mi >> 1)));
-                MmaType<T>::mma(acc[2 * dp], pa, bv[0], bv[1]);
-                MmaType<T>::mma(acc[2 * dp + 1], pa, bv[2], bv[3]);
-            }
+            bad |= (bad_stages >> now & 1u) != 0;
+            attend_block<T, D>(qa, ring + static_cast<uint32_t>(now) * (2 * BLK),
+                               it.t * kTile + warp * TOK, it.len, scale_log2, w);
             __syncwarp();                           // the stage may be refilled
-        }
-        cp_async_wait_all_groups();
+            now = now + 1 == kStages ? 0 : now + 1;
+            if (++it.t < it.n_tiles && left > 1)
+                continue;
 
-        // ---- the four warps' (m, l, O) into one
-        l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
-        l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
-        l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
-        l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-        if (__any_sync(0xffffffffu, bad)) {         // a bad page or length: NaN
-            l_a = l_b = __int_as_float(0x7fc00000);
-            if (lane == 0)
-                atomicOr(&g_error_attention_decode, kErrBadIndex);
-        }
-        if ((lane & 3) == 0) {
-            sm_m[warp][r_a] = m_a;
-            sm_m[warp][r_a + 8] = m_b;
-            sm_l[warp][r_a] = l_a;
-            sm_l[warp][r_a + 8] = l_b;
-        }
-        __syncthreads();                            // and every warp's ring is free
-        float M_a = kNegInf, M_b = kNegInf;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            M_a = fmaxf(M_a, sm_m[w][r_a]);
-            M_b = fmaxf(M_b, sm_m[w][r_a + 8]);
-        }
-        const float f_a = M_a == kNegInf ? 0.0f : ex2_ftz(m_a - M_a);
-        const float f_b = M_b == kNegInf ? 0.0f : ex2_ftz(m_b - M_b);
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-            float* const a = sm_o + (warp * kRows + r_a) * D + i * 8 + c_q;
-            *reinterpret_cast<float2*>(a) = make_float2(acc[i][0] * f_a, acc[i][1] * f_a);
-            *reinterpret_cast<float2*>(a + 8 * D) = make_float2(acc[i][2] * f_b, acc[i][3] * f_b);
-        }
-        __syncthreads();
-        // Row r, columns c .. c + 3 of the four warps' sum, with its (m, l).
-        auto sum_of = [&](int r, int c, float& M, float& L) {
-            M = kNegInf;
-            L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                M = fmaxf(M, sm_m[w][r]);
-            const float ref = M == kNegInf ? 0.0f : M;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                L += sm_l[w][r] * ex2_ftz(sm_m[w][r] - ref);
-                const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * kRows + r) * D + c);
-                o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+            // ---- the piece ends: its four warps' sums into one
+            const ItemHeads heads(sh, it.in);
+            const int64_t seq = it.seq;
+            const bool whole = from == 0 && it.t == it.n_tiles;
+            Part<D>* const part = parts + 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+            if (from == 0 && !whole) {
+                // The run that holds the item's last tile.
+                const int64_t last = it.first + it.n_tiles - 1;
+                begun_item = seq * inner + it.in;
+                int64_t c = last * run.runs / run.total;
+                while (run.total * (c + 1) / run.runs <= last)
+                    ++c;
+                while (run.total * c / run.runs > last)
+                    --c;
+                begun_last = c;
             }
-            return o;
-        };
-        auto store = [&](int r, int c, const float4& o, float M, float L) {
-            const float inv = 1.0f / L;
-            uint2 w2;
-            w2.x = Elem<T>::pack2(o.x * inv, o.y * inv);
-            w2.y = Elem<T>::pack2(o.z * inv, o.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.o.data) + seq * p.o.row +
-                                      static_cast<int64_t>(h0 + r) * p.o.head + c) = w2;
-            if (p.lse && c == 0)
-                p.lse[seq * p.n_heads + h0 + r] =
-                    L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
-        };
-        if constexpr (CLUSTER) {
-            // Each CTA leaves its sum in the place of warp 0's; then CTA r
-            // merges every cluster-th group of four columns of all of them, in
-            // the order of the CTAs.
-            namespace cg = cooperative_groups;
-            if (sh.cluster > 1) {
-                float M[kRows * D / 4 / kThreads], L[kRows * D / 4 / kThreads];
-                float4 o[kRows * D / 4 / kThreads];
+            if (left > 1) {                         // the next item's Q meanwhile
+                it.next_item(p, inner);
+                from = 0;
+                const ItemHeads next(sh, it.in);
+                load_q<D>(p, it.seq, next.h0, next.rows, qa);
+            }
+            w.close(bad);
+            const int r_a = lane >> 2, c_q = (lane & 3) * 2;
 #pragma unroll
-                for (int j = 0; j < kRows * D / 4 / kThreads; ++j) {
-                    const int i = tid + j * kThreads;
-                    o[j] = sum_of(i / (D / 4), (i % (D / 4)) * 4, M[j], L[j]);
+            for (int half = 0; half < 2; ++half) {
+                const int rows = heads.rows - half * 8 < 8 ? heads.rows - half * 8 : 8;
+                if (rows <= 0)
+                    break;
+                __syncthreads();                    // sm_o (and stats) have been read
+                if (half == 0)
+                    stats.put(w);
+                if (r_a < rows) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+                        *reinterpret_cast<float2*>(sm_o + (warp * 8 + r_a) * D + i * 8 + c_q) =
+                            make_float2(w.acc[i][half * 2], w.acc[i][half * 2 + 1]);
                 }
                 __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kRows * D / 4 / kThreads; ++j) {
-                    const int i = tid + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
-                    *reinterpret_cast<float4*>(sm_o + r * D + c) = o[j];
-                    if (c == 0) {
-                        sm_m[0][r] = M[j];
-                        sm_l[0][r] = L[j];
-                    }
-                }
-                cg::cluster_group cluster = cg::this_cluster();
-                cluster.sync();
-                for (int i = crank + tid * sh.cluster; i < rows * (D / 4);
-                     i += kThreads * sh.cluster) {
-                    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-                    float Mx = kNegInf, Lx = 0.0f;
-                    for (int q = 0; q < sh.cluster; ++q)
-                        Mx = fmaxf(Mx, *cluster.map_shared_rank(&sm_m[0][r], q));
-                    const float ref = Mx == kNegInf ? 0.0f : Mx;
-                    float4 acc4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int q = 0; q < sh.cluster; ++q) {
-                        const float f = ex2_ftz(*cluster.map_shared_rank(&sm_m[0][r], q) - ref);
-                        const float4 x = *reinterpret_cast<const float4*>(
-                            cluster.map_shared_rank(sm_o + r * D + c, q));
-                        Lx += *cluster.map_shared_rank(&sm_l[0][r], q) * f;
-                        acc4.x += x.x * f; acc4.y += x.y * f; acc4.z += x.z * f; acc4.w += x.w * f;
-                    }
-                    store(r, c, acc4, Mx, Lx);
-                }
-                cluster.sync();                     // read before a CTA leaves
-            } else {
                 for (int i = tid; i < rows * (D / 4); i += kThreads) {
-                    float M, L;
-                    const float4 o = sum_of(i / (D / 4), (i % (D / 4)) * 4, M, L);
-                    store(i / (D / 4), (i % (D / 4)) * 4, o, M, L);
+                    const int r = i / (D / 4), c = (i % (D / 4)) * 4, row = half * 8 + r;
+                    const float M = stats.max_of(row);
+                    float L = 0.0f;
+                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int q = 0; q < kWarps; ++q) {
+                        const float f = stats.factor(stats.m[q][row], M);
+                        const float4 x =
+                            *reinterpret_cast<const float4*>(sm_o + (q * 8 + r) * D + c);
+                        // (M of -inf: no score but -inf or NaN, which l holds)
+                        L += stats.l[q][row] * (M == kNegInf ? 1.0f : f);
+                        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+                    }
+                    if (whole) {
+                        store_head<T>(p, seq, heads.h0 + row, c, o, M, L);
+                    } else {
+                        *reinterpret_cast<float4*>(part->o + row * D + c) = o;
+                        if (c == 0) {
+                            part->m[row] = M;
+                            part->l[row] = L;
+                        }
+                    }
                 }
             }
-            return;
+            w.clear();
+            bad = it.bad;
         }
-        const bool whole = t0 == 0 && t1 == nt;
-        Part<D>* const part = parts + 2 * static_cast<int64_t>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            float M, L;
-            const float4 o = sum_of(r, c, M, L);
-            if (whole) {
-                store(r, c, o, M, L);
-            } else {
-                *reinterpret_cast<float4*>(part->o + r * D + c) = o;
-                if (c == 0) {
-                    part->m[r] = M;
-                    part->l[r] = L;
-                }
-            }
-        }
-        if (!whole && t0 == 0) {
-            // The run that holds the item's last tile.
-            const int64_t last = first + nt - 1;
-            begun_item = seq * inner + in;
-            int64_t c = last * run.runs / run.total;
-            while (run.total * (c + 1) / run.runs <= last)
-                ++c;
-            while (run.total * c / run.runs > last)
-                --c;
-            begun_last = c;
-        }
-        at = first + t1;
-        __syncthreads();                            // sm_o is a ring again
+        cp_async_wait_all_groups();
     }
     if (tid == 0)
         begun[blockIdx.x] = Begun{begun_item, begun_last};
@@ -538,81 +781,116 @@ attention_decode_kernel(const DecodeProblem p, const DecodeShape sh, float scale
 
 // Merge the parts of the item that CTA blockIdx.x of the main kernel began
 // and did not end: slot 1 of that CTA, then slot 0 of each CTA up to the last.
-// A warp per query head.
+// A thread takes four columns of a row; threads left over take every G-th
+// part, and their sums are merged in order.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+struct JoinSum {
+    float m, l;
+    float4 o;
+
+    __device__ __forceinline__ void clear()
+    {
+        m = kNegInf;
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+
+    __device__ __forceinline__ void read(const Part<D>* q, int r, int c)
+    {
+        m = q->m[r];
+        l = q->l[r];
+        o = *reinterpret_cast<const float4*>(q->o + r * D + c);
+    }
+
+    __device__ __forceinline__ void merge(const JoinSum& x)
+    {
+        const float M = fmaxf(m, x.m), ref = M == kNegInf ? 0.0f : M;
+        const float f = ex2_ftz(m - ref), g = ex2_ftz(x.m - ref);
+        m = M;
+        l = l * f + x.l * g;
+        o.x = o.x * f + x.o.x * g;
+        o.y = o.y * f + x.o.y * g;
+        o.z = o.z * f + x.o.z * g;
+        o.w = o.w * f + x.o.w * g;
+    }
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kRows * 32)
+__global__ void __launch_bounds__(kJoinThreads)
 attention_decode_join_kernel(const DecodeProblem p, const DecodeShape sh)
 {
-    constexpr int E = D / 32;                       // elements per lane
-    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    __shared__ JoinSum<D> sums[kJoinThreads];
+    const int tid = threadIdx.x;
     const Part<D>* const parts = static_cast<const Part<D>*>(p.workspace);
     const Begun* const begun =
         reinterpret_cast<const Begun*>(parts + 2 * static_cast<int64_t>(sh.grid));
-    pdl_launch_dependents();
-    pdl_wait();
-    const Begun g = begun[blockIdx.x];
-    if (g.item < 0)
-        return;
-    const int inner = p.cache.n_kv_heads * sh.blocks;
-    const int64_t seq = g.item / inner;
-    const int in = static_cast<int>(g.item - seq * inner);
-    const int kvh = in / sh.blocks, hb = in - kvh * sh.blocks;
-    const int rows = sh.group - hb * kRows < kRows ? sh.group - hb * kRows : kRows;
-    if (r >= rows)
-        return;
-    const int n = static_cast<int>(g.last - blockIdx.x) + 1;
     auto part = [&](int i) {
         return parts + 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0);
     };
-    float M = kNegInf;
-    for (int i = lane; i < n; i += 32)
-        M = fmaxf(M, part(i)->m[r]);
-    M = warp_max(M);
-    const float ref = M == kNegInf ? 0.0f : M;
-    float L = 0.0f, o[E];
+    const int inner = p.cache.n_kv_heads * sh.blocks;
+    // Units (row, four columns) of an item with all its rows: items with
+    // fewer leave some threads idle.
+    const int most = (sh.group < kRows ? sh.group : kRows) * (D / 4);
+    const int groups = kJoinThreads / most > 0 ? kJoinThreads / most : 1;
+    pdl_launch_dependents();
+    pdl_wait();
+    const Begun g = begun[blockIdx.x];
+    const int n = static_cast<int>(g.last - blockIdx.x) + 1;
+    for (int u0 = 0; u0 < most; u0 += kJoinThreads) {
+        const int u = u0 + (groups > 1 ? tid % most : tid), mine = groups > 1 ? tid / most : 0;
+        const bool on = u < most && mine < groups;
+        const int r = u / (D / 4), c = (u % (D / 4)) * 4;
+        // This group's first part is read beside the header: an item that was
+        // begun and not ended has two parts at least.
+        JoinSum<D> s, x[4];
+        s.clear();
+        if (on && mine < 2 && blockIdx.x + mine < gridDim.x)
+            s.read(part(mine), r, c);
+        if (g.item < 0)
+            return;
+        const int64_t seq = g.item / inner;
+        const ItemHeads heads(sh, static_cast<int>(g.item - seq * inner));
+        if (on && r < heads.rows) {
+            int i = mine;
+            if (mine < 2)
+                i += groups;
+            else
+                s.clear();
+            for (; i < n; i += 4 * groups) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        o[e] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const Part<D>* const q = part(i);
-        const float f = ex2_ftz(q->m[r] - ref);
-        L += q->l[r] * f;
-        float x[E];
-        if constexpr (E == 4) {
-            const float4 w = *reinterpret_cast<const float4*>(q->o + r * D + lane * E);
-            x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(q->o + r * D + lane * E);
-            x[0] = w.x; x[1] = w.y;
+                for (int k = 0; k < 4; ++k)
+                    if (i + k * groups < n)
+                        x[k].read(part(i + k * groups), r, c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i + k * groups < n)
+                        s.merge(x[k]);
+            }
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] += x[e] * f;
+        if (groups > 1) {
+            sums[tid] = s;
+            __syncthreads();
+            if (mine == 0)
+                for (int k = 1; k < groups && k < n; ++k)
+                    s.merge(sums[k * most + u]);
+        }
+        if (on && mine == 0 && r < heads.rows)
+            store_head<T>(p, seq, heads.h0 + r, c, s.o, s.m, s.l);
     }
-    const float inv = 1.0f / L;
-    const int h = kvh * sh.group + hb * kRows + r;
-    unsigned* const dst = reinterpret_cast<unsigned*>(
-        static_cast<unsigned short*>(p.o.data) + seq * p.o.row +
-        static_cast<int64_t>(h) * p.o.head + lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        dst[e / 2] = Elem<T>::pack2(o[e] * inv, o[e + 1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[seq * p.n_heads + h] =
-            L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 template <typename T, int D>
 cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
 {
-    const DecodeShape sh = decode_shape(p.n_seqs, p.n_heads, p.cache.n_kv_heads, p.cache.capacity,
+    const DecodeShape sh = decode_shape(p.n_seqs, p.n_heads, p.cache.n_kv_heads, D, p.cache.capacity,
                                         sm_count_current());
-    auto* kern = sh.cluster > 0 ? attention_decode_kernel<T, D, true>
-                                : attention_decode_kernel<T, D, false>;
-    const int smem = kWarps * kStages * 2 * kWarpTokens * D * 2;
-    static_assert(kWarps * kRows * D * 4 <= kWarps * kStages * 2 * kWarpTokens * D * 2,
-                  "the warps' O rows fit in the rings");
+    auto* kern = sh.cluster > 0 ? attention_decode_cluster_kernel<T, D>
+                                : attention_decode_runs_kernel<T, D>;
+    constexpr int kRing = kWarps * kStages * 2 * warp_tokens(D) * D * 2;
+    static_assert(kWarps * kRows * D * 4 <= kRing, "the warps' O rows fit in the rings");
+    const int smem = kRing + (sh.cluster > 0 ? 0 : kWarps * 8 * D * 4);
     static std::atomic<bool> attr_set[2][64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
@@ -639,7 +917,7 @@ cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
     note_launch();
     if (err != cudaSuccess || sh.cluster > 0)
         return err;
-    cfg.blockDim = dim3(kRows * 32, 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     err = cudaLaunchKernelEx(&cfg, attention_decode_join_kernel<T, D>, p, sh);
     note_launch();
@@ -651,7 +929,7 @@ cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
 size_t attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int64_t n_kv_heads,
                                   int64_t head_dim, int64_t capacity)
 {
-    const DecodeShape sh = decode_shape(n_seqs, n_heads, n_kv_heads, capacity, sm_count_current());
+    const DecodeShape sh = decode_shape(n_seqs, n_heads, n_kv_heads, head_dim, capacity, sm_count_current());
     if (sh.cluster > 0)
         return 0;
     const size_t part = head_dim == 64 ? sizeof(Part<64>) : sizeof(Part<128>);

@@ -50,6 +50,9 @@ struct PagedCache {
     int64_t n_seqs, table_stride;
     int32_t n_pages, table_width, n_kv_heads, capacity;      // capacity: tokens of a table row
     Divisor page;
+    // K and V have the same strides, and every row begins less than 2^31 units
+    // of 16 bytes into its cache.
+    bool near_rows;
 };
 
 struct AppendProblem {

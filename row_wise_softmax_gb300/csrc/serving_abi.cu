@@ -128,7 +128,10 @@ int check_cache(const softmax_paged_cache_t& c, PagedCache* out)
                       static_cast<int32_t>(c.n_pages), static_cast<int32_t>(c.table_width),
                       static_cast<int32_t>(c.n_kv_heads),
                       static_cast<int32_t>(c.table_width * c.page_size),
-                      divisor_of(static_cast<uint32_t>(c.page_size))};
+                      divisor_of(static_cast<uint32_t>(c.page_size)), false};
+    out->near_rows = c.k_page_stride == c.v_page_stride && c.k_row_stride == c.v_row_stride &&
+                     (c.n_pages - 1) * c.k_page_stride + (c.page_size - 1) * c.k_row_stride <
+                         (int64_t{8} << 31);
     return SOFTMAX_OK;
 }
 
