@@ -13,6 +13,7 @@ allocated for that stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -100,30 +101,36 @@ def _cache(name, k, v, table, dtype, device):
                   table.data_ptr(), rows, width, step if rows > 1 else width)
 
 
-def _device_of(name, t):
-    """t's CUDA device index and the dtype code of its dtype."""
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError("%s: dtype must be bfloat16 or float16, got %s" % (name, t.dtype))
-    device = t.get_device()
+_current = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(name, device, stream, call):
+    """call() with CUDA device ``device`` and ``stream`` (a torch stream, a raw
+    handle, or None: the device's current one) current, so that what it
+    allocates is allocated for that stream."""
     if device < 0:
         raise ValueError("%s: expects CUDA tensors" % name)
-    return device, code
-
-
-def _on(device, stream, run):
-    """run(handle) on ``stream`` (a torch stream, a raw handle, or None: the
-    device's current one), with its device current and allocations made for
-    it.  Returns what run returns."""
-    if stream is None and torch._C._cuda_getDevice() == device:
-        return run(torch._C._cuda_getCurrentRawStream(device))
     with torch.cuda.device(device):
         if stream is None:
-            return run(torch.cuda.current_stream(device).cuda_stream)
+            return call()
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
-            return run(stream.cuda_stream)
+            return call()
+
+
+def _code(name, dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("%s: dtype must be bfloat16 or float16, got %s" % (name, dtype))
+    return code
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(device, b, h, hk, d, capacity):
+    """Workspace bytes of a decode call of these sizes (``device``: current)."""
+    return _lib().softmax_attention_decode_workspace(b, h, hk, d, capacity)
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=None, q_out=None,
@@ -145,46 +152,50 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
     tensor), or None without q.
     """
     name = "kv_append"
+    device = k.get_device()
+    if stream is not None or device != _current():
+        return _elsewhere(name, device, stream, lambda: kv_append(
+            k, v, k_cache, v_cache, page_table, positions, seq_ids, q, q_out, inv_freq,
+            interleaved))
     if k.dim() != 3 or k.shape != v.shape:
         raise ValueError("kv_append: k and v must be [tokens, kv_heads, head_dim]")
     n, hk, d = k.shape
-    device, code = _device_of(name, k)
     dtype = k.dtype
+    code = _code(name, dtype)
     cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
-    if k_cache.shape[2:] != (hk, d):
+    if k_cache.shape[2] != hk or k_cache.shape[3] != d:
         raise ValueError("kv_append: the cache's heads do not match k")
-    ks, vs = _heads(name, "k", k, dtype, device), _heads(name, "v", v, dtype, device)
     pos = _index(name, "positions", positions, n, device)
+    ids = None
     if seq_ids is not None:
         ids = _index(name, "seq_ids", seq_ids, n, device)
-    else:
-        ids = None
-        if page_table.shape[0] < n:
-            raise ValueError("kv_append: page_table has fewer rows than there are tokens")
+    elif page_table.shape[0] < n:
+        raise ValueError("kv_append: page_table has fewer rows than there are tokens")
     rot, freq = 0, None
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != device or \
                 inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("kv_append: inv_freq must be a float64 vector on cuda:%d" % device)
         rot, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    h, qs = 0, None
+    h, qs, qo = 0, None, None
     if q is not None:
         if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
             raise ValueError("kv_append: q must be [tokens, heads, head_dim]")
-        h, qs = q.shape[1], _heads(name, "q", q, dtype, device)
-    if q_out is not None and (q is None or q_out.shape != q.shape):
-        raise ValueError("kv_append: q_out must match q")
-
-    def run(handle):
-        out = torch.empty_like(q) if q is not None and q_out is None else q_out
-        qo = None if out is None else _heads(name, "q_out", out, dtype, device)
-        st = _lib().softmax_kv_append(cache, ks, vs, qs, qo, h, pos, ids, n, freq, rot,
-                                      1 if interleaved else 0, code, handle)
-        if st != OK:
-            raise SoftmaxError(st, name)
-        return out
-
-    return _on(device, stream, run)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        elif q_out.shape != q.shape:
+            raise ValueError("kv_append: q_out must match q")
+        h = q.shape[1]
+        qs = _heads(name, "q", q, dtype, device)
+        qo = _heads(name, "q_out", q_out, dtype, device)
+    elif q_out is not None:
+        raise ValueError("kv_append: q_out without q")
+    st = (_declared or _lib()).softmax_kv_append(
+        cache, _heads(name, "k", k, dtype, device), _heads(name, "v", v, dtype, device), qs, qo, h,
+        pos, ids, n, freq, rot, 1 if interleaved else 0, code, _raw_stream(device))
+    if st != OK:
+        raise SoftmaxError(st, name)
+    return q_out
 
 
 def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | None = None,
@@ -202,37 +213,37 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
     float32 [sequences, heads].
     """
     name = "attention_decode"
+    device = q.get_device()
+    if stream is not None or device != _current():
+        return _elsewhere(name, device, stream, lambda: attention_decode(
+            q, k_cache, v_cache, page_table, lengths, scale, out, return_lse))
     if q.dim() != 3:
         raise ValueError("attention_decode: q must be [sequences, heads, head_dim]")
     b, h, d = q.shape
-    device, code = _device_of(name, q)
     dtype = q.dtype
+    code = _code(name, dtype)
     cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
     _, size, hk, dim = k_cache.shape
     if dim != d or hk == 0 or h == 0 or h % hk:
         raise ValueError("attention_decode: the cache's heads do not match q")
-    if page_table.shape[0] != b:
+    rows, width = page_table.shape
+    if rows != b:
         raise ValueError("attention_decode: page_table must have a row for each query")
-    qs = _heads(name, "q", q, dtype, device)
     lens = _index(name, "lengths", lengths, b, device)
-    if out is not None and out.shape != q.shape:
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
         raise ValueError("attention_decode: out must match q")
-
-    def run(handle):
-        o = torch.empty_like(q) if out is None else out
-        os = _heads(name, "out", o, dtype, device)
-        lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
-        L = _lib()
-        need = L.softmax_attention_decode_workspace(b, h, hk, d, page_table.shape[1] * size)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-        st = L.softmax_attention_decode(cache, qs, os, lse.data_ptr() if return_lse else None, h,
-                                        lens, d ** -0.5 if scale is None else scale, code,
-                                        ws.data_ptr() if need > 0 else None, max(need, 0), handle)
-        if st != OK:
-            raise SoftmaxError(st, name)
-        return (o, lse) if return_lse else o
-
-    return _on(device, stream, run)
+    lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
+    need = _decode_workspace(device, b, h, hk, d, width * size)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    st = (_declared or _lib()).softmax_attention_decode(
+        cache, _heads(name, "q", q, dtype, device), _heads(name, "out", out, dtype, device),
+        lse.data_ptr() if return_lse else None, h, lens, d ** -0.5 if scale is None else scale,
+        code, ws.data_ptr() if need > 0 else None, need if need > 0 else 0, _raw_stream(device))
+    if st != OK:
+        raise SoftmaxError(st, name)
+    return (out, lse) if return_lse else out
 
 
 def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causal: bool = True,
@@ -252,35 +263,35 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     (out, lse) with lse float32 [total_q, heads].
     """
     name = "attention_packed"
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[2] != k.shape[2]:
+    device = q.get_device()
+    if stream is not None or device != _current():
+        return _elsewhere(name, device, stream, lambda: attention_packed(
+            q, k, v, cu_q, cu_k, scale, causal, out, return_lse))
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape:
         raise ValueError("attention_packed: q must be [total_q, heads, head_dim], k and v "
                          "[total_k, kv_heads, head_dim]")
     n, h, d = q.shape
-    m, hk, _ = k.shape
-    if h == 0 or hk == 0 or h % hk:
-        raise ValueError("attention_packed: heads must be a multiple of kv_heads")
-    device, code = _device_of(name, q)
+    m, hk, dim = k.shape
+    if dim != d or h == 0 or hk == 0 or h % hk:
+        raise ValueError("attention_packed: heads must be a multiple of kv_heads, and head_dim "
+                         "the same")
     dtype = q.dtype
-    qs, ks, vs = (_heads(name, "q", q, dtype, device), _heads(name, "k", k, dtype, device),
-                  _heads(name, "v", v, dtype, device))
+    code = _code(name, dtype)
     seqs = cu_q.numel() - 1
     if seqs < 0:
         raise ValueError("attention_packed: cu_q must be a vector of sequences + 1 bounds")
     cq = _index(name, "cu_q", cu_q, seqs + 1, device)
     ck = cq if cu_k is None else _index(name, "cu_k", cu_k, seqs + 1, device)
-    if out is not None and out.shape != q.shape:
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
         raise ValueError("attention_packed: out must match q")
-
-    def run(handle):
-        o = torch.empty_like(q) if out is None else out
-        os = _heads(name, "out", o, dtype, device)
-        lse = torch.empty((n, h), dtype=torch.float32, device=q.device) if return_lse else None
-        st = _lib().softmax_attention_packed(qs, ks, vs, os,
-                                             lse.data_ptr() if return_lse else None, cq, ck, seqs,
-                                             n, m, h, hk, d, d ** -0.5 if scale is None else scale,
-                                             1 if causal else 0, code, handle)
-        if st != OK:
-            raise SoftmaxError(st, name)
-        return (o, lse) if return_lse else o
-
-    return _on(device, stream, run)
+    lse = torch.empty((n, h), dtype=torch.float32, device=q.device) if return_lse else None
+    st = (_declared or _lib()).softmax_attention_packed(
+        _heads(name, "q", q, dtype, device), _heads(name, "k", k, dtype, device),
+        _heads(name, "v", v, dtype, device), _heads(name, "out", out, dtype, device),
+        lse.data_ptr() if return_lse else None, cq, ck, seqs, n, m, h, hk, d,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, code, _raw_stream(device))
+    if st != OK:
+        raise SoftmaxError(st, name)
+    return (out, lse) if return_lse else out
