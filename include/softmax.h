@@ -365,7 +365,7 @@ int64_t softmax_attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int6
  *   cu_q, cu_k n_seqs + 1 int32 each, rising (cu_k may be cu_q).  A sequence
  *              whose bounds fall or leave [0, total] is skipped
  *              (SOFTMAX_ERR_DEVICE_INDEX).  Rows of o in no sequence are left
- *              as they were.
+ *              as they were, rows in two hold either's result.
  *   A query that sees no key gives NaN (lse = -inf).  Values that a query
  *   does not see have no influence on it, whatever they hold.
  *   total_q and total_k below 2^31.

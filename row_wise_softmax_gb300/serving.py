@@ -153,7 +153,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
     """
     name = "kv_append"
     device = k.get_device()
-    if stream is not None or device != _current():
+    if stream is not None or device < 0 or device != _current():
         return _elsewhere(name, device, stream, lambda: kv_append(
             k, v, k_cache, v_cache, page_table, positions, seq_ids, q, q_out, inv_freq,
             interleaved))
@@ -214,7 +214,7 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
     """
     name = "attention_decode"
     device = q.get_device()
-    if stream is not None or device != _current():
+    if stream is not None or device < 0 or device != _current():
         return _elsewhere(name, device, stream, lambda: attention_decode(
             q, k_cache, v_cache, page_table, lengths, scale, out, return_lse))
     if q.dim() != 3:
@@ -264,7 +264,7 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     """
     name = "attention_packed"
     device = q.get_device()
-    if stream is not None or device != _current():
+    if stream is not None or device < 0 or device != _current():
         return _elsewhere(name, device, stream, lambda: attention_packed(
             q, k, v, cu_q, cu_k, scale, causal, out, return_lse))
     if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape:

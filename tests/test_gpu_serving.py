@@ -130,6 +130,96 @@ def test_decode(i, dtype):
     decode_case(*DECODE[i], dtype, 100 + i)
 
 
+@pytest.mark.parametrize("i", range(len(DECODE)))
+def test_decode_behind_a_wide_table(i):
+    """The same through the kernels of long calls: a table with room for far
+    more tokens than there are decides the launch."""
+    lengths, h, hk, d, page = DECODE[i]
+    decode_case(lengths, h, hk, d, page, torch.bfloat16, 130 + i, width=400000 // page + 1)
+
+
+@pytest.mark.parametrize("width", [None, 40000])
+def test_decode_different_strides_of_k_and_v(width):
+    g = rng(9)
+    lengths, page, hk, d = [90, 200, 7], 16, 2, 128
+    k, _, table = paged(g, lengths, page, hk, d, torch.bfloat16, width=width)
+    _, v, _ = paged(g, lengths, page, hk, d, torch.bfloat16, heads_first=True)
+    v = v[:k.shape[0]]
+    q = normal(g, 3, 8, d, dtype=torch.bfloat16)
+    o = rws.attention_decode(q, k, v, torch.from_numpy(table).cuda(), ints(lengths))
+    close(o, None, ref.decode(f64(q), f64(k), f64(v), table, lengths, d ** -0.5), q.dtype, 200)
+
+
+@pytest.mark.parametrize("group", [48, 128])
+@pytest.mark.parametrize("width", [None, 40000])
+def test_decode_many_heads_to_one(group, width):
+    decode_case([300, 5], group, 1, 64, 16, torch.bfloat16, 10, width=width)
+
+
+def test_decode_strided_in_place_and_lse_only_rows():
+    """q a part of a projection's output, out = q, and a scale."""
+    g = rng(11)
+    lengths, page, h, hk, d = [100, 0, 33], 16, 4, 2, 128
+    k, v, table = paged(g, lengths, page, hk, d, torch.float16)
+    wide = normal(g, 3, h + 2, d, dtype=torch.float16)
+    q, rest = wide[:, :h], wide[:, h:].clone()
+    want = ref.decode(f64(q), f64(k), f64(v), table, lengths, 0.3)
+    o, lse = rws.attention_decode(q, k, v, torch.from_numpy(table).cuda(), ints(lengths), scale=0.3,
+                                  out=q, return_lse=True)
+    assert o is q and torch.equal(wide[:, h:], rest)
+    close(o, lse, want, torch.float16, 100)
+
+
+@pytest.mark.parametrize("width", [16, 40000])
+def test_decode_bad_pages_and_lengths(width):
+    """A sequence with a bad page or length gives NaN and a status; the others
+    are as ever, and a bad page past a sequence's length is not looked at."""
+    g = rng(12)
+    lengths, page, h, hk, d = [200, 64, 130, 50, 9], 16, 8, 2, 128
+    k, v, table = paged(g, lengths, page, hk, d, torch.bfloat16, width=width)
+    q = normal(g, 5, h, d, dtype=torch.bfloat16)
+    want = ref.decode(f64(q), f64(k), f64(v), table, lengths, d ** -0.5)
+    table[1, 3] = k.shape[0]                        # the first page that is not there
+    table[2, 0] = -1
+    table[4, 1] = 1 << 30                           # past the length
+    n = list(lengths)
+    n[3] = width * page + 1
+    for bad in (n[3], -1):
+        n[3] = bad
+        o, lse = rws.attention_decode(q, k, v, torch.from_numpy(table).cuda(), ints(n),
+                                      return_lse=True)
+        assert bool(torch.isnan(o[1:4]).all()) and bool(torch.isnan(lse[1:3]).all())
+        ok = [0, 4]
+        close(o[ok], lse[ok], [w[ok] for w in want], torch.bfloat16, 200)
+        assert rws.device_status(clear=False) == rws.ERR_DEVICE_INDEX
+        assert rws.device_status() == rws.ERR_DEVICE_INDEX
+        assert rws.device_status() == rws.OK
+
+
+def test_decode_far_pages():
+    """Rows more than 2^31 elements into the caches."""
+    page, hk, d = 16, 8, 128
+    pages = (1 << 31) // (page * hk * d) + 40
+    k = torch.empty(pages, page, hk, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    g = rng(13)
+    for c in (k, v):
+        c[-30:] = normal(g, 30, page, hk, d, dtype=torch.bfloat16)
+    table = (pages - 30 + np.random.default_rng(1).permutation(30)).astype(np.int32).reshape(2, 15)
+    q = normal(g, 2, 16, d, dtype=torch.bfloat16)
+    lengths = [240, 177]
+    got = rws.attention_decode(q, k, v, torch.from_numpy(table).cuda(), ints(lengths))
+    near = table - (pages - 30)
+    close(got, None, ref.decode(f64(q), f64(k[-30:]), f64(v[-30:]), near, lengths, d ** -0.5),
+          q.dtype, 240)
+    pos = ints([241, 180])
+    k2, v2 = (normal(g, 2, hk, d, dtype=torch.bfloat16) for _ in range(2))
+    table = np.concatenate([table, [[pages - 1], [pages - 2]]], 1).astype(np.int32)
+    rws.kv_append(k2, v2, k, v, torch.from_numpy(table).cuda(), pos)
+    assert torch.equal(k[pages - 1, 1], k2[0]) and torch.equal(v[table[1, 11], 4], v2[1])
+    assert rws.device_status() == rws.OK
+
+
 def test_decode_heads_first_pages_and_wide_table():
     decode_case([130, 77, 1], 8, 2, 128, 16, torch.bfloat16, 7, heads_first=True, width=40)
 
@@ -176,6 +266,108 @@ PACKED = [  # n_q, n_k, heads, kv_heads, head_dim, causal, fused
 def test_packed(i, dtype):
     n_q, n_k, h, hk, d, causal, fused = PACKED[i]
     packed_case(n_q, n_k, h, hk, d, causal, dtype, 200 + i, fused)
+
+
+def test_packed_many_sequences():
+    """More sequences than the kernel ranks by length, and units that see no key."""
+    r = np.random.default_rng(3)
+    n_q = [int(x) for x in r.integers(0, 40, 300)]
+    n_k = [max(0, n + int(r.integers(-8, 30))) for n in n_q]
+    packed_case(n_q, n_k, 4, 2, 64, True, torch.bfloat16, 81)
+    packed_case(n_q, n_k, 2, 1, 128, False, torch.float16, 82)
+
+
+@pytest.mark.parametrize("group", [32, 48, 128])
+def test_packed_many_heads_to_one(group):
+    packed_case([70, 3], [70, 100], group, 1, 128, True, torch.bfloat16, 83)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_packed_unseen_values_have_no_influence(d, bad, in_place):
+    """Keys and values of other sequences, behind the last one, and past the
+    diagonal hold NaN or infinity: a query that does not see them is as if
+    they were not there; one that does has them in its output."""
+    g = rng(84)
+    lens, h, hk, dtype = [150, 70, 200], 4, 2, torch.bfloat16
+    cu = np.cumsum([0] + lens)
+    t = cu[-1]
+    q = normal(g, t + 9, h, d, dtype=dtype)
+    k, v = (normal(g, t + 9, hk, d, dtype=dtype) for _ in range(2))
+    k[cu[1]:cu[2]] = bad                            # the sequence between
+    v[cu[1]:cu[2]] = bad
+    k[t:], v[t:] = bad, bad
+    v[cu[2] + 130] = bad                            # a later token of the last
+    v[90, 0, 3] = bad                               # one value of a token of the first
+    want, _, mag = ref.packed(f64(q), f64(k), np.where(np.isfinite(f64(v)), f64(v), 0.0), cu, cu,
+                              d ** -0.5, True)
+    out = q.clone() if in_place else torch.full_like(q, 3.0)
+    o = rws.attention_packed(out if in_place else q, k, v, ints(cu), causal=True, out=out)
+    got = f64(o)
+    assert np.array_equal(got[t:], f64(q)[t:] if in_place else np.full(got[t:].shape, 3.0))
+    seen = np.zeros(got.shape, bool)                # outputs that such a value reaches
+    seen[90:cu[1], :h // hk, 3] = True
+    seen[cu[1]:cu[2]] = True
+    seen[cu[2] + 130:t] = True
+    seen[t:] = True
+    assert np.all(np.isfinite(got[~seen]))
+    bound = (2.0 ** -8 + 2.0 ** -14) * mag + 2.0 ** -8 * np.abs(want) + 2.0 ** -24
+    assert np.all(np.abs(got - want)[~seen] <= bound[~seen])
+    seen[t:] = False
+    assert not np.any(np.isfinite(got[seen]))
+    assert rws.device_status() == rws.OK
+
+
+def test_packed_rows_in_no_sequence_stay():
+    g = rng(85)
+    h, hk, d, dtype = 2, 1, 128, torch.float16
+    q = normal(g, 400, h, d, dtype=dtype)
+    k, v = (normal(g, 400, hk, d, dtype=dtype) for _ in range(2))
+    cu = np.array([17, 100, 100, 333])
+    out = torch.full_like(q, -5.0)
+    o, lse = rws.attention_packed(q, k, v, ints(cu), out=out, return_lse=True)
+    want = ref.packed(f64(q), f64(k), f64(v), cu, cu, d ** -0.5, True)
+    close(o[17:333], lse[17:333], [w[17:333] for w in want], dtype, 233)
+    assert bool((out[:17] == -5).all()) and bool((out[333:] == -5).all())
+
+
+def test_packed_bad_bounds():
+    g = rng(86)
+    h, d, dtype = 2, 64, torch.bfloat16
+    q, k, v = (normal(g, 300, h, d, dtype=dtype) for _ in range(3))
+    good = np.array([0, 50, 120, 200, 300])
+    want, _, mag = ref.packed(f64(q), f64(k), f64(v), good, good, d ** -0.5, True)
+    # (Rows 40 to 49 of the first lie in two sequences: either's.)
+    for cu, ok in ((np.array([0, 50, 40, 200, 300]), [(0, 40), (200, 300)]),
+                   (np.array([0, 50, 120, 301, 1 << 30]), [(0, 50), (50, 120)]),
+                   (np.array([-3, 50, 120, 200, 300]), [(50, 120), (120, 200), (200, 300)])):
+        out = torch.full_like(q, 9.0)
+        rws.attention_packed(q, k, v, ints(cu), out=out)
+        assert rws.device_status() == rws.ERR_DEVICE_INDEX
+        got = f64(out)
+        for a, b in ok:
+            bound = 2.0 ** -7 * (mag + np.abs(want)) + 1e-6
+            assert np.all(np.abs(got - want)[a:b] <= bound[a:b])
+    assert rws.device_status() == rws.OK
+
+
+def test_packed_repeated_and_missing_keys():
+    """Heads of K and V that are one in memory (stride 0), and no key at all."""
+    g = rng(87)
+    n, h, d, dtype = 60, 4, 64, torch.bfloat16
+    q = normal(g, n, h, d, dtype=dtype)
+    k1, v1 = (normal(g, n, 1, d, dtype=dtype) for _ in range(2))
+    cu = np.array([0, 25, 60])
+    o, lse = rws.attention_packed(q, k1.expand(n, 2, d), v1.expand(n, 2, d), ints(cu),
+                                  return_lse=True)
+    two = [np.repeat(f64(x), 2, 1) for x in (k1, v1)]
+    close(o, lse, ref.packed(f64(q), *two, cu, cu, d ** -0.5, True), dtype, 35)
+    none = torch.empty(0, 2, d, dtype=dtype, device="cuda")
+    o, lse = rws.attention_packed(q, none, none, ints([0, 25, 60]), ints([0, 0, 0]), causal=False,
+                                  return_lse=True)
+    assert bool(torch.isnan(o).all()) and bool((lse == float("-inf")).all())
+    assert rws.device_status() == rws.OK
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -305,3 +497,174 @@ def test_append_packed_prompts_padding_and_in_place():
     pos[[3, 50]] = -1                               # padding
     append_case(len(ids), 4, 2, 64, 64, False, 16, torch.bfloat16, 32, positions=pos,
                 seq_ids=ids, n_seqs=3, in_place=True)
+
+
+def test_append_bad_indexes_write_nothing():
+    """Bad sequences, positions and pages: a status, and no cache row but the
+    good token's changes; queries are turned all the same."""
+    g = rng(40)
+    page, hk, d, dtype = 8, 2, 64, torch.bfloat16
+    kc, vc = (normal(g, 4, page, hk, d, dtype=dtype) for _ in range(2))
+    k, v = (normal(g, 6, hk, d, dtype=dtype) for _ in range(2))
+    q = normal(g, 6, 3, d, dtype=dtype)
+    table = ints([[0, 1], [2, 4], [-1, 3]])
+    ids, pos = ints([0, 7, -1, 1, 2, 0]), ints([3, 0, 0, 8, 1, 16])
+    before_k, before_v = kc.clone(), vc.clone()
+    inv = torch.ones(8, dtype=torch.float64, device="cuda")
+    out = rws.kv_append(k, v, kc, vc, table, pos, ids, q=q, inv_freq=inv)
+    assert rws.device_status() == rws.ERR_DEVICE_INDEX and rws.device_status() == rws.OK
+    want = ref.rotate(f64(k), [3] * 6, np.ones(8), False)[0]
+    assert np.all(np.abs(f64(kc[0, 3]) - want) <= 2.0 ** -8 * np.abs(want) + 1e-5)
+    assert torch.equal(vc[0, 3], v[0])
+    kc[0, 3], vc[0, 3] = before_k[0, 3], before_v[0, 3]
+    assert torch.equal(kc, before_k) and torch.equal(vc, before_v)
+    want = ref.rotate(f64(q), pos.tolist(), np.ones(8), False)
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + 1e-5)
+
+
+def test_append_into_one_interleaved_cache_tensor():
+    g = rng(41)
+    cache = torch.zeros(5, 2, 16, 2, 128, dtype=torch.float16, device="cuda")
+    k, v = (normal(g, 20, 2, 128, dtype=torch.float16) for _ in range(2))
+    rws.kv_append(k, v, cache[:, 0], cache[:, 1], ints([[3, 1]]), ints(list(range(20))),
+                  ints([0] * 20))
+    assert torch.equal(cache[3, 0], k[:16]) and torch.equal(cache[3, 1], v[:16])
+    assert torch.equal(cache[1, 0, :4], k[16:]) and torch.equal(cache[1, 1, :4], v[16:])
+    assert not cache[1, :, 4:].any() and not cache[[0, 2, 4]].any()
+
+
+# ------------------------------------------------------------- together
+def test_prompt_then_steps():
+    """Prompts through kv_append and attention_packed, then three decoding
+    steps, against one attention over everything in float64."""
+    g = rng(50)
+    lens, steps, h, hk, d, page = [37, 1, 130], 3, 8, 2, 128, 16
+    dtype, e = torch.bfloat16, HALF_STEP[torch.bfloat16]
+    b, cu = len(lens), np.cumsum([0] + lens)
+    inv = 10000.0 ** (-np.arange(d // 2) / (d // 2))
+    freq = torch.tensor(inv, device="cuda")
+    width = -(-(max(lens) + steps) // page)
+    table = torch.randperm(b * width, generator=g, device="cuda").int().view(b, width)
+    kc = torch.full((b * width, page, hk, d), float("nan"), dtype=dtype, device="cuda")
+    vc = kc.clone()
+    qkv = normal(g, int(cu[-1]), h + 2 * hk, d, dtype=dtype)
+    ids = np.repeat(np.arange(b), lens)
+    pos = np.concatenate([np.arange(n) for n in lens])
+    q = rws.kv_append(qkv[:, h:h + hk], qkv[:, h + hk:], kc, vc, table, ints(pos), ints(ids),
+                      q=qkv[:, :h], inv_freq=freq)
+    keys = torch.stack([kc[table[s, p // page], p % page] for s, p in zip(ids, pos)])
+    values = torch.stack([vc[table[s, p // page], p % page] for s, p in zip(ids, pos)])
+    assert torch.equal(values, qkv[:, h + hk:])
+    out = rws.attention_packed(q, keys, values, ints(cu))
+    close(out, None, ref.packed(f64(q), f64(keys), f64(values), cu, cu, d ** -0.5, True), dtype, 130)
+    now = list(lens)
+    for _ in range(steps):
+        qkv = normal(g, b, h + 2 * hk, d, dtype=dtype)
+        q = rws.kv_append(qkv[:, h:h + hk], qkv[:, h + hk:], kc, vc, table, ints(now), q=qkv[:, :h],
+                          inv_freq=freq)
+        turned = ref.rotate(f64(qkv[:, :h]), now, inv, False)
+        assert np.all(np.abs(f64(q) - turned) <= e * np.abs(turned) + 1e-5)
+        now = [n + 1 for n in now]
+        out = rws.attention_decode(q, kc, vc, table, ints(now))
+        close(out, None, ref.decode(f64(q), f64(kc), f64(vc), table.cpu().numpy(), now, d ** -0.5),
+              dtype, max(now))
+    assert rws.device_status() == rws.OK
+
+
+def everything(g, dtype=torch.bfloat16):
+    """Inputs of one call of each operator, and the call."""
+    lens = [70, 300, 5]
+    k, v, table = paged(g, [4000, 90, 0, 700], 16, 2, 128, dtype, width=20000)
+    s = dict(k=k, v=v, table=torch.from_numpy(table).cuda(), lengths=ints([4000, 90, 0, 700]),
+             q=normal(g, 4, 8, 128, dtype=dtype), pq=normal(g, 375, 8, 128, dtype=dtype),
+             pk=normal(g, 375, 2, 128, dtype=dtype), pv=normal(g, 375, 2, 128, dtype=dtype),
+             cu=ints(np.cumsum([0] + lens)), kc=torch.zeros_like(k), vc=torch.zeros_like(v),
+             pos=ints([7, 30, -1, 16]), freq=torch.rand(64, dtype=torch.float64, device="cuda"))
+
+    def call(stream=None):
+        return (rws.attention_decode(s["q"], s["k"], s["v"], s["table"], s["lengths"],
+                                     stream=stream),
+                rws.attention_decode(s["q"], s["k"], s["v"], s["table"][:, :250].contiguous(),
+                                     s["lengths"], stream=stream),
+                rws.attention_packed(s["pq"], s["pk"], s["pv"], s["cu"], stream=stream),
+                rws.kv_append(s["pk"][:4], s["pv"][:4], s["kc"], s["vc"], s["table"], s["pos"],
+                              q=s["q"], inv_freq=s["freq"], stream=stream)[:2],
+                s["kc"], s["vc"])
+    return s, call
+
+
+def test_same_bits_on_every_run_and_stream():
+    s, call = everything(rng(51))
+    want = [x.clone() for x in call()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        got = [call(st) for st in streams] + [call(st.cuda_stream) for st in streams]
+        torch.cuda.synchronize()
+        for outs in got:
+            for a, b in zip(outs, want):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_graph_replay_reads_new_lengths():
+    """Two graphs that hold the same calls, replayed side by side with other
+    lengths, bounds and inputs than were captured."""
+    s, call = everything(rng(52))
+    call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = call()[:3]
+        graphs.append((graph, outs, torch.cuda.Stream()))
+    s["lengths"].copy_(ints([100, 3999, 64, 0]))
+    s["table"].copy_(torch.where(s["table"] < 0, 0, s["table"]))
+    s["cu"].copy_(ints([10, 11, 200, 375]))
+    s["q"].mul_(0.5)
+    want = [x.clone() for x in call()[:3]]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, _, st in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+    for _, outs, _ in graphs:
+        for n, (a, b) in enumerate(zip(outs, want)):
+            if n == 2:                              # rows before cu[0] are nobody's
+                a, b = a[10:], b[10:]
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16)), n
+
+
+def test_binding_checks():
+    s, _ = everything(rng(53))
+    cpu = s["q"].cpu()
+    with pytest.raises(ValueError):
+        rws.attention_decode(cpu, s["k"], s["v"], s["table"], s["lengths"])
+    with pytest.raises(ValueError):
+        rws.attention_decode(s["q"], s["k"].cpu(), s["v"], s["table"], s["lengths"])
+    with pytest.raises(TypeError):
+        rws.attention_decode(s["q"].float(), s["k"], s["v"], s["table"], s["lengths"])
+    with pytest.raises(ValueError):
+        rws.attention_decode(s["q"], s["k"], s["v"], s["table"].long(), s["lengths"])
+    with pytest.raises(ValueError):
+        rws.attention_decode(s["q"], s["k"], s["v"], s["table"], s["lengths"][:3])
+    with pytest.raises(ValueError):
+        rws.attention_packed(s["pq"][:, :3], s["pk"], s["pv"], s["cu"])
+    with pytest.raises(ValueError):
+        rws.attention_packed(s["pq"], s["pk"], s["pv"], s["cu"].long())
+    with pytest.raises(rws.SoftmaxError):           # a head_dim that is not offered
+        rws.attention_packed(*(s[x][..., :96].contiguous() for x in ("pq", "pk", "pv")), s["cu"])
+    with pytest.raises(rws.SoftmaxError):           # out over k
+        rws.attention_packed(s["pk"], s["pk"], s["pv"], s["cu"], out=s["pv"])
+    with pytest.raises(ValueError):
+        rws.kv_append(s["pk"][:5], s["pv"][:5], s["kc"], s["vc"], s["table"], ints([0] * 5))
+    with pytest.raises(rws.SoftmaxError):           # rot_dim past head_dim
+        rws.kv_append(s["pk"][:4], s["pv"][:4], s["kc"], s["vc"], s["table"], s["pos"],
+                      inv_freq=torch.ones(72, dtype=torch.float64, device="cuda"))
+    before = rws.launch_count()
+    rws.attention_packed(s["pq"][:0], s["pk"], s["pv"], ints([0, 0]), ints([0, 375]))
+    rws.attention_decode(s["q"][:0], s["k"], s["v"], s["table"][:0], s["lengths"][:0])
+    rws.kv_append(s["pk"][:0], s["pv"][:0], s["kc"], s["vc"], s["table"], s["pos"][:0])
+    assert rws.launch_count() == before             # nothing to do
+    assert rws.device_status() == rws.OK
