@@ -70,6 +70,7 @@ struct Begun {
 struct DecodeShape {
     int32_t group, blocks;                          // heads per kv head, 16-head blocks of them
     int32_t grid, cluster;
+    int32_t abreast;                                // run form: items that a CTA walks side by side
 };
 
 constexpr int kMaxCluster = 16;
@@ -86,6 +87,7 @@ inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, i
     const int64_t most = static_cast<int64_t>(sm_count) * kCtasPerSm;
     const int64_t items = n_seqs * n_kv * s.blocks;
     s.cluster = 0;
+    s.abreast = 1;
     if (items <= most) {
         int c = 1;
         while (c < kMaxCluster && c < per && items * c * 2 <= most)
@@ -96,7 +98,18 @@ inline DecodeShape decode_shape(int64_t n_seqs, int64_t n_heads, int64_t n_kv, i
             return s;
         }
     }
-    s.grid = static_cast<int32_t>(items >= most || items * per >= most ? most : items * per);
+    // D = 64 and enough items to fill the device: a warp to an item, so that
+    // a CTA reads up to four heads' 128-byte rows of a token together (200 x
+    // 1000 tokens of 16 heads: 129 us against 133 to 145 one item at a time).
+    // 256-byte rows gain nothing from it (61 ragged sequences up to 8192: 104
+    // against 101 us), nor do few items (1 x 2000: 12.5 against 9.0 us).
+    if (head_dim == 64 && items >= most)
+        while (s.abreast < kWarps && n_kv * s.blocks % (2 * s.abreast) == 0)
+            s.abreast *= 2;
+    const int64_t groups = items / s.abreast;
+    const int64_t tile_run = tile / kWarps * (kWarps / s.abreast);
+    const int64_t runs = capacity > 0 ? (capacity + tile_run - 1) / tile_run : 1;
+    s.grid = static_cast<int32_t>(groups >= most || groups * runs >= most ? most : groups * runs);
     return s;
 }
 
@@ -523,6 +536,12 @@ attention_decode_cluster_kernel(const DecodeProblem p, const DecodeShape sh, flo
 }
 
 // ------------------------------------------------------- equal runs of tiles
+// A CTA walks `HW` items side by side (key/value heads of one sequence: their
+// rows of a token lie next to each other in memory), TW = kWarps / HW warps to
+// each of them, which take turns of warp_tokens tokens.  A tile is
+// TW * warp_tokens tokens of HW items.  Sequences without tokens have no
+// tiles; their outputs are written apart.
+
 // A CTA's run [begin, end) of all tiles, and the sequence it begins in.
 struct Run {
     int64_t begin, end;                             // tiles
@@ -531,17 +550,21 @@ struct Run {
     int64_t before;                                 // tiles of the sequences before it
 };
 
+template <int TILE>
+__device__ __forceinline__ int32_t run_tiles(int32_t n)
+{
+    return (n + TILE - 1) / TILE;
+}
+
 // Every thread gets the same answer.  The sequences' tiles are summed 128 at a
 // time; with no more sequences than that, one pass finds total and place.
-template <int D>
-__device__ Run find_run(const DecodeProblem& p, int inner, Run& place, int64_t* scratch)
+template <int TILE, int LEAST>
+__device__ Run find_run(const DecodeProblem& p, int groups, Run& place, int64_t* scratch)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto scan = [&](int64_t b, int64_t& upto) {     // tiles of sequence b, and of the block up to it
         bool bad = false;
-        const int64_t n = b < p.n_seqs ? tiles_of<D>(length_of(p, b, bad)) : 0;
-        if (bad && blockIdx.x == 0)
-            atomicOr(&g_error_attention_decode, kErrBadIndex);
+        const int64_t n = b < p.n_seqs ? run_tiles<TILE>(length_of(p, b, bad)) : 0;
         upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -553,13 +576,10 @@ __device__ Run find_run(const DecodeProblem& p, int inner, Run& place, int64_t* 
         if (lane == 31)
             scratch[warp] = upto;
         __syncthreads();
-        int64_t all = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w)
             if (w < warp)
                 upto += scratch[w];
-            all += scratch[w];
-        }
         return n;
     };
     auto all = [&] {
@@ -575,20 +595,22 @@ __device__ Run find_run(const DecodeProblem& p, int inner, Run& place, int64_t* 
         n = scan(b + tid, upto);
         total += all();
     }
-    // No run is empty but those of the CTAs past the last tile: an item's
-    // parts lie in consecutive CTAs.
-    r.total = total * inner;
-    r.runs = r.total < gridDim.x ? r.total : gridDim.x;
+    // Runs of LEAST tiles at least (short ones cost more to join than they
+    // save), and none that is empty but those of the CTAs past the last: an
+    // item's parts lie in consecutive CTAs.
+    r.total = total * groups;
+    r.runs = (r.total + LEAST - 1) / LEAST;
+    r.runs = r.runs < gridDim.x ? r.runs : gridDim.x;
     r.begin = blockIdx.x < r.runs ? r.total * blockIdx.x / r.runs : 0;
     r.end = blockIdx.x < r.runs ? r.total * (blockIdx.x + 1) / r.runs : 0;
     int64_t before = 0;
     for (int64_t b = 0; b < p.n_seqs; b += kThreads) {
         if (p.n_seqs > kThreads)
             n = scan(b + tid, upto);
-        if (r.begin < r.end && n > 0 && (before + upto - n) * inner <= r.begin &&
-            r.begin < (before + upto) * inner) {
+        if (r.begin < r.end && n > 0 && (before + upto - n) * groups <= r.begin &&
+            r.begin < (before + upto) * groups) {
             place.seq = b + tid;
-            place.before = (before + upto - n) * inner;
+            place.before = (before + upto - n) * groups;
         }
         before += all();
     }
@@ -598,17 +620,17 @@ __device__ Run find_run(const DecodeProblem& p, int inner, Run& place, int64_t* 
     return r;
 }
 
-// A place in the order of all tiles: tile t of item (seq, in).
-template <int D>
+// A place in the order of all tiles: tile t of head group g of a sequence.
+template <int TILE>
 struct Cursor {
-    int64_t seq, first;                             // first: the item's first tile among all
-    int32_t in, t, n_tiles, len;
-    bool bad;                                       // the length is
+    int64_t seq, first;                             // first: the group's first tile among all
+    int32_t g, t, n_tiles, len;
 
     __device__ __forceinline__ void read(const DecodeProblem& p)
     {
+        bool bad;
         len = length_of(p, seq, bad);
-        n_tiles = tiles_of<D>(len);
+        n_tiles = run_tiles<TILE>(len);
     }
 
     __device__ __forceinline__ void begin(const DecodeProblem& p, const Run& run)
@@ -616,29 +638,31 @@ struct Cursor {
         seq = run.seq;
         read(p);
         const int64_t at = run.begin - run.before;
-        in = static_cast<int32_t>(at / n_tiles);
-        t = static_cast<int32_t>(at - static_cast<int64_t>(in) * n_tiles);
-        first = run.before + static_cast<int64_t>(in) * n_tiles;
+        g = static_cast<int32_t>(at / n_tiles);
+        t = static_cast<int32_t>(at - static_cast<int64_t>(g) * n_tiles);
+        first = run.before + static_cast<int64_t>(g) * n_tiles;
     }
 
-    // To the next item (there must be one).
-    __device__ __forceinline__ void next_item(const DecodeProblem& p, int inner)
+    // To the next group that has tiles (there must be one).
+    __device__ __forceinline__ void next_group(const DecodeProblem& p, int groups)
     {
         first += n_tiles;
         t = 0;
-        if (++in == inner) {
-            in = 0;
-            ++seq;
-            read(p);
+        if (++g == groups) {
+            g = 0;
+            do {
+                ++seq;
+                read(p);
+            } while (n_tiles == 0);
         }
     }
 };
 
-template <typename T, int D>
+template <typename T, int D, int HW>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float scale_log2)
 {
-    constexpr int TOK = warp_tokens(D), kTile = tile_tokens(D);
+    constexpr int TOK = warp_tokens(D), TW = kWarps / HW, TILE = TOK * TW;
     constexpr uint32_t BLK = TOK * D * 2;           // bytes of a warp's K (or V) block
     extern __shared__ __align__(128) unsigned char dec_smem[];
     __shared__ RowStats stats;
@@ -646,38 +670,52 @@ attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float 
     __shared__ Run sm_place;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int inner = p.cache.n_kv_heads * sh.blocks;
+    const int hw = warp % HW, tw = warp / HW;
+    const int inner = p.cache.n_kv_heads * sh.blocks, groups = inner / HW;
     const uint32_t ring = smem_addr(dec_smem) + warp * (kStages * 2 * BLK);
-    // Eight rows of every warp's O: half an item at a time, beside the rings,
-    // which go on filling.
+    // TW > 1: eight rows of every warp's O, half an item at a time, beside the
+    // rings, which go on filling.
     float* const sm_o = reinterpret_cast<float*>(dec_smem + kWarps * kStages * 2 * BLK);
     Part<D>* const parts = static_cast<Part<D>*>(p.workspace);
-    Begun* const begun = reinterpret_cast<Begun*>(parts + 2 * static_cast<int64_t>(sh.grid));
+    Begun* const begun = reinterpret_cast<Begun*>(parts + 2 * HW * static_cast<int64_t>(sh.grid));
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * HW + hw;    // of parts / 2 and begun
 
     pdl_launch_dependents();
     pdl_wait();
-    const Run run = find_run<D>(p, inner, sm_place, sm_scratch);
+    const Run run = find_run<TILE, HW>(p, groups, sm_place, sm_scratch);
+    // Sequences without tokens, dealt to the CTAs: NaN (0 / 0).
+    for (int64_t b = blockIdx.x; b < p.n_seqs; b += gridDim.x) {
+        bool bad;
+        if (length_of(p, b, bad) > 0)
+            continue;
+        if (bad && tid == 0)
+            atomicOr(&g_error_attention_decode, kErrBadIndex);
+        const float nan = __int_as_float(0x7fc00000);
+        for (int i = tid; i < p.n_heads * (D / 4); i += kThreads)
+            store_head<T>(p, b, i / (D / 4), (i % (D / 4)) * 4, make_float4(nan, nan, nan, nan),
+                          kNegInf, bad ? nan : 0.0f);
+    }
     int64_t begun_item = -1, begun_last = 0;
     if (run.begin < run.end) {
         // Two cursors walk the run: one copies, kStages - 1 tiles ahead and on
         // into the next items, the other computes.
-        Cursor<D> copy, it;
+        Cursor<TILE> copy, it;
         it.begin(p, run);
         copy = it;
         int64_t to_copy = run.end - run.begin;
         uint32_t bad_stages = 0;
-        const int32_t tok0 = warp * TOK + lane % TOK;
+        const int32_t tok0 = tw * TOK + lane % TOK;
         auto copy_next = [&](int st) {
             if (to_copy > 0) {
                 --to_copy;
-                const int32_t t = copy.t * kTile;
+                const int32_t t = copy.t * TILE;
                 const bool bad = copy_block<D>(
-                    p, copy.in / sh.blocks, t + warp * TOK,
+                    p, (copy.g * HW + hw) / sh.blocks, t + tw * TOK,
                     page_of(p, p.cache.table + copy.seq * p.cache.table_stride, t + tok0, copy.len),
                     copy.len, ring + static_cast<uint32_t>(st) * (2 * BLK));
                 bad_stages = (bad_stages & ~(1u << st)) | (bad ? 1u << st : 0u);
                 if (++copy.t == copy.n_tiles && to_copy > 0)
-                    copy.next_item(p, inner);
+                    copy.next_group(p, groups);
             }
             cp_async_commit();
         };
@@ -686,12 +724,12 @@ attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float 
             copy_next(i);
         uint32_t qa[D / 16][4];
         {
-            const ItemHeads heads(sh, it.in);
+            const ItemHeads heads(sh, it.g * HW + hw);
             load_q<D>(p, it.seq, heads.h0, heads.rows, qa);
         }
         WarpSum<D> w;
         w.clear();
-        bool bad = it.bad;
+        bool bad = false;
         int32_t from = it.t;                        // the piece's first tile
         int now = 0;                                // the stage of the tile at hand
         for (int64_t left = run.end - run.begin; left > 0; --left) {
@@ -700,21 +738,21 @@ attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float 
             __syncwarp();
             bad |= (bad_stages >> now & 1u) != 0;
             attend_block<T, D>(qa, ring + static_cast<uint32_t>(now) * (2 * BLK),
-                               it.t * kTile + warp * TOK, it.len, scale_log2, w);
+                               it.t * TILE + tw * TOK, it.len, scale_log2, w);
             __syncwarp();                           // the stage may be refilled
             now = now + 1 == kStages ? 0 : now + 1;
             if (++it.t < it.n_tiles && left > 1)
                 continue;
 
-            // ---- the piece ends: its four warps' sums into one
-            const ItemHeads heads(sh, it.in);
+            // ---- the piece ends
+            const ItemHeads heads(sh, it.g * HW + hw);
             const int64_t seq = it.seq;
             const bool whole = from == 0 && it.t == it.n_tiles;
-            Part<D>* const part = parts + 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+            Part<D>* const part = parts + 2 * mine + (from == 0 ? 1 : 0);
             if (from == 0 && !whole) {
                 // The run that holds the item's last tile.
                 const int64_t last = it.first + it.n_tiles - 1;
-                begun_item = seq * inner + it.in;
+                begun_item = seq * inner + it.g * HW + hw;
                 int64_t c = last * run.runs / run.total;
                 while (run.total * (c + 1) / run.runs <= last)
                     ++c;
@@ -723,64 +761,103 @@ attention_decode_runs_kernel(const DecodeProblem p, const DecodeShape sh, float 
                 begun_last = c;
             }
             if (left > 1) {                         // the next item's Q meanwhile
-                it.next_item(p, inner);
+                it.next_group(p, groups);
                 from = 0;
-                const ItemHeads next(sh, it.in);
+                const ItemHeads next(sh, it.g * HW + hw);
                 load_q<D>(p, it.seq, next.h0, next.rows, qa);
             }
             w.close(bad);
             const int r_a = lane >> 2, c_q = (lane & 3) * 2;
+            if constexpr (TW == 1) {
+                // The warp's sum is the item's.
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int rows = heads.rows - half * 8 < 8 ? heads.rows - half * 8 : 8;
-                if (rows <= 0)
-                    break;
-                __syncthreads();                    // sm_o (and stats) have been read
-                if (half == 0)
-                    stats.put(w);
-                if (r_a < rows) {
+                for (int half = 0; half < 2; ++half) {
+                    const int row = half * 8 + r_a;
+                    const float M = half == 0 ? w.m_a : w.m_b, L = half == 0 ? w.l_a : w.l_b;
+                    if (row < heads.rows) {
+                        if (whole) {
+                            const float inv = 1.0f / L;
+                            unsigned short* const o = static_cast<unsigned short*>(p.o.data) +
+                                seq * p.o.row + static_cast<int64_t>(heads.h0 + row) * p.o.head + c_q;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i)
-                        *reinterpret_cast<float2*>(sm_o + (warp * 8 + r_a) * D + i * 8 + c_q) =
-                            make_float2(w.acc[i][half * 2], w.acc[i][half * 2 + 1]);
-                }
-                __syncthreads();
-                for (int i = tid; i < rows * (D / 4); i += kThreads) {
-                    const int r = i / (D / 4), c = (i % (D / 4)) * 4, row = half * 8 + r;
-                    const float M = stats.max_of(row);
-                    float L = 0.0f;
-                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int i = 0; i < D / 8; ++i)
+                                *reinterpret_cast<unsigned*>(o + i * 8) =
+                                    Elem<T>::pack2(w.acc[i][half * 2] * inv,
+                                                   w.acc[i][half * 2 + 1] * inv);
+                            if (p.lse && c_q == 0)
+                                p.lse[seq * p.n_heads + heads.h0 + row] =
+                                    L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+                        } else {
 #pragma unroll
-                    for (int q = 0; q < kWarps; ++q) {
-                        const float f = stats.factor(stats.m[q][row], M);
-                        const float4 x =
-                            *reinterpret_cast<const float4*>(sm_o + (q * 8 + r) * D + c);
-                        // (M of -inf: no score but -inf or NaN, which l holds)
-                        L += stats.l[q][row] * (M == kNegInf ? 1.0f : f);
-                        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+                            for (int i = 0; i < D / 8; ++i)
+                                *reinterpret_cast<float2*>(part->o + row * D + i * 8 + c_q) =
+                                    make_float2(w.acc[i][half * 2], w.acc[i][half * 2 + 1]);
+                            if (c_q == 0) {
+                                part->m[row] = M;
+                                part->l[row] = L;
+                            }
+                        }
                     }
-                    if (whole) {
-                        store_head<T>(p, seq, heads.h0 + row, c, o, M, L);
-                    } else {
-                        *reinterpret_cast<float4*>(part->o + row * D + c) = o;
-                        if (c == 0) {
-                            part->m[row] = M;
-                            part->l[row] = L;
+                }
+            } else {
+                // The TW warps' sums into one, in the order of the warps.
+                const int most = sh.group < kRows ? sh.group : kRows;    // rows of any item
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (half * 8 >= most)
+                        break;
+                    __syncthreads();                // sm_o (and stats) have been read
+                    if (half == 0)
+                        stats.put(w);
+                    if (half * 8 + r_a < heads.rows) {
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i)
+                            *reinterpret_cast<float2*>(sm_o + (warp * 8 + r_a) * D + i * 8 + c_q) =
+                                make_float2(w.acc[i][half * 2], w.acc[i][half * 2 + 1]);
+                    }
+                    __syncthreads();
+                    const int rows = heads.rows - half * 8 < 8 ? heads.rows - half * 8 : 8;
+                    for (int i = tw * 32 + lane; i < rows * (D / 4); i += TW * 32) {
+                        const int r = i / (D / 4), c = (i % (D / 4)) * 4, row = half * 8 + r;
+                        float M = kNegInf, L = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < TW; ++q)
+                            M = fmaxf(M, stats.m[q * HW + hw][row]);
+                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                        for (int q = 0; q < TW; ++q) {
+                            const int v = q * HW + hw;
+                            const float f = stats.factor(stats.m[v][row], M);
+                            const float4 x =
+                                *reinterpret_cast<const float4*>(sm_o + (v * 8 + r) * D + c);
+                            // (M of -inf: no score but -inf or NaN, which l holds)
+                            L += stats.l[v][row] * (M == kNegInf ? 1.0f : f);
+                            o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+                        }
+                        if (whole) {
+                            store_head<T>(p, seq, heads.h0 + row, c, o, M, L);
+                        } else {
+                            *reinterpret_cast<float4*>(part->o + row * D + c) = o;
+                            if (c == 0) {
+                                part->m[row] = M;
+                                part->l[row] = L;
+                            }
                         }
                     }
                 }
             }
             w.clear();
-            bad = it.bad;
+            bad = false;
         }
         cp_async_wait_all_groups();
     }
-    if (tid == 0)
-        begun[blockIdx.x] = Begun{begun_item, begun_last};
+    if (tw == 0 && lane == 0)
+        begun[mine] = Begun{begun_item, begun_last};
 }
 
 // Merge the parts of the item that CTA blockIdx.x of the main kernel began
-// and did not end: slot 1 of that CTA, then slot 0 of each CTA up to the last.
+// and did not end, abreast place blockIdx.y: slot 1 of that CTA, then slot 0 of
+// each CTA up to the last.
 // A thread takes four columns of a row; threads left over take every G-th
 // part, and their sums are merged in order.
 constexpr int kJoinThreads = 256;
@@ -825,9 +902,10 @@ attention_decode_join_kernel(const DecodeProblem p, const DecodeShape sh)
     const int tid = threadIdx.x;
     const Part<D>* const parts = static_cast<const Part<D>*>(p.workspace);
     const Begun* const begun =
-        reinterpret_cast<const Begun*>(parts + 2 * static_cast<int64_t>(sh.grid));
+        reinterpret_cast<const Begun*>(parts + 2 * sh.abreast * static_cast<int64_t>(sh.grid));
     auto part = [&](int i) {
-        return parts + 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0);
+        return parts + 2 * ((static_cast<int64_t>(blockIdx.x) + i) * sh.abreast + blockIdx.y) +
+               (i == 0 ? 1 : 0);
     };
     const int inner = p.cache.n_kv_heads * sh.blocks;
     // Units (row, four columns) of an item with all its rows: items with
@@ -836,7 +914,7 @@ attention_decode_join_kernel(const DecodeProblem p, const DecodeShape sh)
     const int groups = kJoinThreads / most > 0 ? kJoinThreads / most : 1;
     pdl_launch_dependents();
     pdl_wait();
-    const Begun g = begun[blockIdx.x];
+    const Begun g = begun[static_cast<int64_t>(blockIdx.x) * sh.abreast + blockIdx.y];
     const int n = static_cast<int>(g.last - blockIdx.x) + 1;
     for (int u0 = 0; u0 < most; u0 += kJoinThreads) {
         const int u = u0 + (groups > 1 ? tid % most : tid), mine = groups > 1 ? tid / most : 0;
@@ -886,23 +964,30 @@ cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
 {
     const DecodeShape sh = decode_shape(p.n_seqs, p.n_heads, p.cache.n_kv_heads, D, p.cache.capacity,
                                         sm_count_current());
-    auto* kern = sh.cluster > 0 ? attention_decode_cluster_kernel<T, D>
-                                : attention_decode_runs_kernel<T, D>;
+    const int form = sh.cluster > 0 ? 0 : sh.abreast;   // 0, or 1, 2 or 4 abreast
+    auto* kern = form == 0 ? attention_decode_cluster_kernel<T, D>
+                           : attention_decode_runs_kernel<T, D, 1>;
+    if constexpr (D == 64) {
+        if (form == 2)
+            kern = attention_decode_runs_kernel<T, D, 2>;
+        else if (form == 4)
+            kern = attention_decode_runs_kernel<T, D, 4>;
+    }
     constexpr int kRing = kWarps * kStages * 2 * warp_tokens(D) * D * 2;
     static_assert(kWarps * kRows * D * 4 <= kRing, "the warps' O rows fit in the rings");
-    const int smem = kRing + (sh.cluster > 0 ? 0 : kWarps * 8 * D * 4);
-    static std::atomic<bool> attr_set[2][64];
+    const int smem = kRing + (form == 1 || form == 2 ? kWarps * 8 * D * 4 : 0);
+    static std::atomic<bool> attr_set[kWarps + 1][64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return cudaErrorInvalidDevice;
-    if (!attr_set[sh.cluster > 0][dev].load()) {
+    if (!attr_set[form][dev].load()) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && sh.cluster > 0)
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
-        attr_set[sh.cluster > 0][dev].store(true);
+        attr_set[form][dev].store(true);
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
@@ -917,6 +1002,7 @@ cudaError_t launch(const DecodeProblem& p, cudaStream_t s)
     note_launch();
     if (err != cudaSuccess || sh.cluster > 0)
         return err;
+    cfg.gridDim = dim3(static_cast<unsigned>(sh.grid), static_cast<unsigned>(sh.abreast), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     err = cudaLaunchKernelEx(&cfg, attention_decode_join_kernel<T, D>, p, sh);
@@ -933,7 +1019,7 @@ size_t attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int64_t n_kv_
     if (sh.cluster > 0)
         return 0;
     const size_t part = head_dim == 64 ? sizeof(Part<64>) : sizeof(Part<128>);
-    return static_cast<size_t>(sh.grid) * (2 * part + sizeof(Begun));
+    return static_cast<size_t>(sh.grid) * sh.abreast * (2 * part + sizeof(Begun));
 }
 
 cudaError_t launch_attention_decode(const DecodeProblem& p, cudaStream_t s)

@@ -121,6 +121,8 @@ DECODE = [  # lengths, heads, kv_heads, head_dim, page
     ([2000, 3, 1999, 64], 12, 4, 128, 64),
     ([20000], 8, 2, 128, 16),                       # one sequence over every CTA
     ([37] * 70, 4, 2, 64, 16),                      # many short ones
+    ([5, 0, 300, 64, 65, 1000, 0, 33] * 12, 8, 4, 64, 16),           # four heads abreast
+    ([5, 0, 300, 64, 65, 1000, 0, 33] * 22, 18, 2, 64, 16),          # two, and two blocks of heads
 ]
 
 
