@@ -53,20 +53,20 @@ def _lib():
     return _declared
 
 
-def _same(name, key, t, dtype, device) -> None:
-    """t lies on CUDA device `device`, has dtype, and contiguous head elements."""
+def _refuse(name, key, t, dtype, device):
+    """What is wrong with a [rows, heads, head_dim] tensor (or a cache)."""
     if t.get_device() != device:
-        raise ValueError("%s: %s must be a tensor on cuda:%d" % (name, key, device))
+        return ValueError("%s: %s must be a tensor on cuda:%d" % (name, key, device))
     if t.dtype is not dtype:
-        raise ValueError("%s: %s must have dtype %s" % (name, key, dtype))
+        return ValueError("%s: %s must have dtype %s" % (name, key, dtype))
+    return ValueError("%s: %s must have contiguous head elements" % (name, key))
 
 
 def _heads(name, key, t, dtype, device):
     """softmax_heads_t of a [rows, heads, head_dim] tensor."""
-    _same(name, key, t, dtype, device)
     row, head, one = t.stride()
-    if one != 1:
-        raise ValueError("%s: %s must have contiguous head elements" % (name, key))
+    if one != 1 or t.dtype is not dtype or t.get_device() != device:
+        raise _refuse(name, key, t, dtype, device)
     return _HEADS(t.data_ptr(), row, head)
 
 
@@ -79,26 +79,26 @@ def _index(name, key, t, n, device):
     return t.data_ptr()
 
 
-def _cache(name, k, v, table, dtype, device):
-    """softmax_paged_cache_t of two caches and a page table."""
-    _same(name, "k_cache", k, dtype, device)
-    _same(name, "v_cache", v, dtype, device)
-    if k.dim() != 4 or k.shape != v.shape:
+def _cache(name, k, v, table, shape, dtype, device):
+    """softmax_paged_cache_t of two caches (``shape``: k's) and a page table."""
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("%s: k_cache and v_cache must be [pages, page_size, kv_heads, head_dim]"
                          % name)
     if table.dtype is not torch.int32 or table.get_device() != device or table.dim() != 2:
         raise ValueError("%s: page_table must be an int32 tensor [sequences, pages] on cuda:%d" %
                          (name, device))
-    pages, size, heads, dim = k.shape
-    rows, width = table.shape
     kp, kr, kh, k1 = k.stride()
     vp, vr, vh, v1 = v.stride()
-    step, t1 = table.stride()
-    if k1 != 1 or v1 != 1 or (width > 1 and t1 != 1):
-        raise ValueError("%s: the caches' head elements and the table's rows must be contiguous"
-                         % name)
-    return _CACHE(k.data_ptr(), v.data_ptr(), pages, size, heads, dim, kp, kr, kh, vp, vr, vh,
-                  table.data_ptr(), rows, width, step if rows > 1 else width)
+    if k1 != 1 or k.dtype is not dtype or k.get_device() != device:
+        raise _refuse(name, "k_cache", k, dtype, device)
+    if v1 != 1 or v.dtype is not dtype or v.get_device() != device:
+        raise _refuse(name, "v_cache", v, dtype, device)
+    rows, width = table.shape
+    step, one = table.stride()
+    if width > 1 and one != 1:
+        raise ValueError("%s: page_table's rows must be contiguous" % name)
+    return _CACHE(k.data_ptr(), v.data_ptr(), *shape, kp, kr, kh, vp, vr, vh, table.data_ptr(),
+                  rows, width, step if rows > 1 else width)
 
 
 _current = torch._C._cuda_getDevice
@@ -157,13 +157,15 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
         return _elsewhere(name, device, stream, lambda: kv_append(
             k, v, k_cache, v_cache, page_table, positions, seq_ids, q, q_out, inv_freq,
             interleaved))
-    if k.dim() != 3 or k.shape != v.shape:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("kv_append: k and v must be [tokens, kv_heads, head_dim]")
-    n, hk, d = k.shape
+    n, hk, d = shape
     dtype = k.dtype
-    code = _code(name, dtype)
-    cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
-    if k_cache.shape[2] != hk or k_cache.shape[3] != d:
+    code = _CODES.get(dtype) or _code(name, dtype)
+    shape = k_cache.shape
+    cache = _cache(name, k_cache, v_cache, page_table, shape, dtype, device)
+    if shape[2] != hk or shape[3] != d:
         raise ValueError("kv_append: the cache's heads do not match k")
     pos = _index(name, "positions", positions, n, device)
     ids = None
@@ -179,13 +181,14 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
         rot, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
     h, qs, qo = 0, None, None
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != d:
             raise ValueError("kv_append: q must be [tokens, heads, head_dim]")
+        h = shape[1]
         if q_out is None:
             q_out = torch.empty_like(q)
-        elif q_out.shape != q.shape:
+        elif q_out.shape != shape:
             raise ValueError("kv_append: q_out must match q")
-        h = q.shape[1]
         qs = _heads(name, "q", q, dtype, device)
         qo = _heads(name, "q_out", q_out, dtype, device)
     elif q_out is not None:
@@ -217,13 +220,15 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
     if stream is not None or device < 0 or device != _current():
         return _elsewhere(name, device, stream, lambda: attention_decode(
             q, k_cache, v_cache, page_table, lengths, scale, out, return_lse))
-    if q.dim() != 3:
+    qshape = q.shape
+    if len(qshape) != 3:
         raise ValueError("attention_decode: q must be [sequences, heads, head_dim]")
-    b, h, d = q.shape
+    b, h, d = qshape
     dtype = q.dtype
-    code = _code(name, dtype)
-    cache = _cache(name, k_cache, v_cache, page_table, dtype, device)
-    _, size, hk, dim = k_cache.shape
+    code = _CODES.get(dtype) or _code(name, dtype)
+    shape = k_cache.shape
+    cache = _cache(name, k_cache, v_cache, page_table, shape, dtype, device)
+    _, size, hk, dim = shape
     if dim != d or hk == 0 or h == 0 or h % hk:
         raise ValueError("attention_decode: the cache's heads do not match q")
     rows, width = page_table.shape
@@ -232,7 +237,7 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
     lens = _index(name, "lengths", lengths, b, device)
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
+    elif out.shape != qshape:
         raise ValueError("attention_decode: out must match q")
     lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
     need = _decode_workspace(device, b, h, hk, d, width * size)
@@ -267,16 +272,17 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     if stream is not None or device < 0 or device != _current():
         return _elsewhere(name, device, stream, lambda: attention_packed(
             q, k, v, cu_q, cu_k, scale, causal, out, return_lse))
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape:
+    qshape, shape = q.shape, k.shape
+    if len(qshape) != 3 or len(shape) != 3 or v.shape != shape:
         raise ValueError("attention_packed: q must be [total_q, heads, head_dim], k and v "
                          "[total_k, kv_heads, head_dim]")
-    n, h, d = q.shape
-    m, hk, dim = k.shape
+    n, h, d = qshape
+    m, hk, dim = shape
     if dim != d or h == 0 or hk == 0 or h % hk:
         raise ValueError("attention_packed: heads must be a multiple of kv_heads, and head_dim "
                          "the same")
     dtype = q.dtype
-    code = _code(name, dtype)
+    code = _CODES.get(dtype) or _code(name, dtype)
     seqs = cu_q.numel() - 1
     if seqs < 0:
         raise ValueError("attention_packed: cu_q must be a vector of sequences + 1 bounds")
@@ -284,7 +290,7 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     ck = cq if cu_k is None else _index(name, "cu_k", cu_k, seqs + 1, device)
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
+    elif out.shape != qshape:
         raise ValueError("attention_packed: out must match q")
     lse = torch.empty((n, h), dtype=torch.float32, device=q.device) if return_lse else None
     st = (_declared or _lib()).softmax_attention_packed(
