@@ -146,28 +146,25 @@ constexpr int kBM = 128;                           // rows of a query tile (TMEM
 constexpr float kLazyRescaleLog2 = 8.0f;           // p <= 2^8 between rescales
 constexpr float kInf = __builtin_inff();
 
-// CTAs that share each product, keys per tile, warps that share a row of S,
-// ring slots of K and of V, CTAs per SM, output columns that a warp stages at
-// a time.
+// CTAs that share each product, keys per tile, ring slots of K and of V.
 template <int D> struct Shape;
 template <> struct Shape<128> {
-    static constexpr int CG = 2, BN = 128, HS = 2, KVS = 3, CTAS = 1, EC = 32;
+    static constexpr int CG = 2, BN = 128, KVS = 3;
 };
 template <> struct Shape<64> {
-    static constexpr int CG = 1, BN = 128, HS = 2, KVS = 4, CTAS = 1, EC = 32;
+    static constexpr int CG = 1, BN = 128, KVS = 4;
 };
+constexpr int kHS = 2;                             // warps that share a row of S
+constexpr int kSoftWarps = 2 * 4 * kHS;            // two query tiles of four TMEM lane groups
+constexpr int kStageBytes = 32 * 64;               // a warp's place for 32 x 32 outputs
 
-template <int D>
-constexpr int packed_threads()
-{
-    return 2 * 4 * Shape<D>::HS * 32 + 96;         // softmax warps, two MMA warps, copy warp
-}
+constexpr int kPackedThreads = (kSoftWarps + 3) * 32;    // softmax, two MMA warps, copy
 
 template <int D>
 constexpr int packed_smem()
 {
     using S = Shape<D>;
-    return (2 * kBM * D + 2 * S::KVS * (S::BN / S::CG) * D) * 2 + 8 * S::HS * 32 * S::EC * 2 + 1024;
+    return (2 * kBM * D + 2 * S::KVS * (S::BN / S::CG) * D) * 2 + kSoftWarps * kStageBytes + 1024;
 }
 
 // The unit of work of a CTA (pair): `tokens` query tokens of one sequence,
@@ -343,14 +340,14 @@ struct UnitFinder {
 };
 
 template <typename T, int D, bool CAUSAL>
-__global__ void __launch_bounds__(packed_threads<D>(), Shape<D>::CTAS)
+__global__ void __launch_bounds__(kPackedThreads, 1)
 attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2)
 {
     using S = Shape<D>;
-    constexpr int CG = S::CG, BN = S::BN, HS = S::HS, KVS = S::KVS, EC = S::EC;
+    constexpr int CG = S::CG, BN = S::BN, KVS = S::KVS, HS = kHS;
     constexpr bool kBF16 = Elem<T>::kNegInfBits == 0xff80u;
     constexpr uint32_t QT_BYTES = kBM * D * 2;               // a query tile
     constexpr uint32_t KV_BYTES = BN / CG * D * 2;           // this CTA's part of a key tile
@@ -361,13 +358,12 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     constexpr uint32_t IDESC_PV = umma_idesc(kBM * CG, D, kBF16, true);
     // Tensor memory: S of either query tile (BN columns), P of each (BN / 2),
     // O of each (D).
-    constexpr uint32_t P_COL = BN, O_COL = 2 * BN, TMEM_COLS = 2 * BN + 2 * D <= 256 ? 256 : 512;
-    static_assert(2 * BN + 2 * D <= 512, "all of tensor memory");
+    constexpr uint32_t P_COL = BN, O_COL = 2 * BN, TMEM_COLS = 512;
+    static_assert(O_COL + 2 * D <= TMEM_COLS, "all of tensor memory");
     constexpr int CW = BN / HS;                              // keys of S per softmax warp
     constexpr int NCH = CW / 32;                             // 32-column chunks per warp
     constexpr int OW = D / HS;                               // O columns per softmax warp
-    constexpr int SOFT = 2 * 4 * HS;                         // softmax warps
-    constexpr int CTRL = SOFT, LOADW = CTRL + 2;             // MMA warps, copy warp
+    constexpr int SOFT = kSoftWarps, CTRL = SOFT, LOADW = CTRL + 2;    // first MMA warp, copy warp
     extern __shared__ __align__(128) unsigned char pk_smem[];
     __shared__ __align__(8) unsigned long long bar_s[2], bar_ld[2], bar_p[2], bar_pv[2];
     __shared__ __align__(8) unsigned long long o_free[2], bar_end, bar_drain[2];
@@ -379,16 +375,16 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     __shared__ Unit s_unit[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int s_failed;
-    __shared__ int s_stop[2][2][4];
+    __shared__ int s_stop[2][2];
     // Row maxima (by tile parity) and final sums of the warps sharing a row,
     // and their rows to be done again.
-    __shared__ float xmax[HS > 1 ? 2 : 1][2][HS][kBM];
+    __shared__ float xmax[2][2][HS][kBM];
     __shared__ float xsum[2][HS][kBM];
     __shared__ unsigned xredo[2][HS][4];
 
     const uint32_t base = (smem_addr(pk_smem) + 1023u) & ~1023u;   // swizzle atoms
     const uint32_t sQ = base, sK = sQ + 2 * QT_BYTES, sV = sK + KVS * KV_BYTES;
-    const uint32_t sO = sV + KVS * KV_BYTES;                 // 32 rows x EC columns per softmax warp
+    const uint32_t sO = sV + KVS * KV_BYTES;                 // kStageBytes per softmax warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank<CG>();
     const int gp = 1 << gp_log2;
@@ -689,18 +685,15 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         const uint32_t bar_weights = leader_addr<CG>(smem_addr(&bar_p[x]));
         const uint32_t bar_over = leader_addr<CG>(smem_addr(&bar_end));
         const uint32_t bar_output = leader_addr<CG>(smem_addr(&o_free[x]));
-        const uint32_t stage = sO + static_cast<uint32_t>(warp * 32 * EC * 2);
-        // With eight warps to a tile one of them waits on the barriers in
-        // shared memory and the others behind it at a named barrier: sixteen
-        // polling warps slow the exponentials down (d = 128, 16384 tokens:
-        // 1677 -> 1744 TFLOP/s).  With four each waits itself (d = 64: 860
-        // against 800).
-        const bool poller = HS == 1 || warp % (4 * HS) == 0;
+        const uint32_t stage = sO + static_cast<uint32_t>(warp * kStageBytes);
+        // One warp of a tile waits on the barriers in shared memory, the
+        // others behind it at a named barrier: sixteen polling warps slow the
+        // exponentials down (d = 128, 16384 tokens: 1677 -> 1744 TFLOP/s).
+        const bool poller = warp % (4 * HS) == 0;
         auto await = [&](int id, unsigned long long* bar, uint32_t parity, bool wait) {
             if (wait && poller)
                 wait1(bar, parity);
-            if constexpr (HS > 1)
-                named_barrier(id, 128 * HS);
+            named_barrier(id, 128 * HS);
         };
         uint32_t done = 0;                                   // key tiles of the units before
         for (uint32_t i = 0;; ++i) {
@@ -710,12 +703,11 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 wait1(&unit_full[i & 1], i >> 1);
                 const int stop = failed_elsewhere();
                 if (lane == 0)
-                    s_stop[i & 1][x][HS == 1 ? warp & 3 : 0] = stop;
+                    s_stop[i & 1][x] = stop;
                 __syncwarp();
             }
-            if constexpr (HS > 1)
-                named_barrier(1 + x, 128 * HS);
-            if (s_stop[i & 1][x][HS == 1 ? warp & 3 : 0])
+            named_barrier(1 + x, 128 * HS);
+            if (s_stop[i & 1][x])
                 break;
             const Unit u = s_unit[i & 1];
             __syncwarp();
@@ -767,15 +759,12 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         mx = max3(mx, sv[c][j], sv[c][j + 1]);
                 // The row's maximum over its HS warps (slots by tile parity);
                 // and P V of the tile before has read P and written O.
-                if constexpr (HS > 1)
-                    xmax[t & 1][x][h][r] = mx;
+                xmax[t & 1][x][h][r] = mx;
                 await(3 + x, &bar_pv[x], done + static_cast<uint32_t>(t - 1), t > 0);
                 tc_fence_after();
-                if constexpr (HS > 1) {
 #pragma unroll
-                    for (int o = 0; o < HS; ++o)
-                        mx = fmaxf(mx, xmax[t & 1][x][o][r]);
-                }
+                for (int o = 0; o < HS; ++o)
+                    mx = fmaxf(mx, xmax[t & 1][x][o][r]);
                 // Lazy rescaling: the reference m (base 2) moves only when the
                 // tile's max exceeds it by more than 2^8; O / l and the
                 // logsumexp only need m and l to agree.
@@ -820,14 +809,12 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 tc_fence_after();
             }
             done += static_cast<uint32_t>(my_kt);
-            if constexpr (HS > 1) {
-                xsum[x][h][r] = l;
-                named_barrier(pair_bar, 32 * HS);
-                l = 0.0f;
+            xsum[x][h][r] = l;
+            named_barrier(pair_bar, 32 * HS);
+            l = 0.0f;
 #pragma unroll
-                for (int o = 0; o < HS; ++o)
-                    l += xsum[x][o][r];
-            }
+            for (int o = 0; o < HS; ++o)
+                l += xsum[x][o][r];
             // A masked key's weight is 0, but 0 times an infinite or NaN value
             // of V is NaN.  Rows with a value of O that is not finite, and
             // such a value in the masked part of their key tiles, are done
@@ -855,15 +842,13 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             // The rows that any of the HS warps found not finite.
             auto not_finite = [&] {
                 unsigned redo = __ballot_sync(0xffffffffu, !(zero0 + zero1 == 0.0f)) & seen;
-                if constexpr (HS > 1) {
-                    if (lane == 0)
-                        xredo[x][h][warp & 3] = redo;
-                    named_barrier(pair_bar, 32 * HS);
+                if (lane == 0)
+                    xredo[x][h][warp & 3] = redo;
+                named_barrier(pair_bar, 32 * HS);
 #pragma unroll
-                    for (int o = 0; o < HS; ++o)
-                        redo |= xredo[x][o][warp & 3];
-                    named_barrier(pair_bar, 32 * HS);        // read before it is written again
-                }
+                for (int o = 0; o < HS; ++o)
+                    redo |= xredo[x][o][warp & 3];
+                named_barrier(pair_bar, 32 * HS);            // read before it is written again
                 return redo;
             };
             const int kvh = u.head / group;
@@ -897,21 +882,19 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             }
             // A row that sees no key is the softmax of only -inf: NaN.
             const float inv = limit > 0 ? 1.0f / l : __int_as_float(0x7fc00000);
-            // EC columns of 32 rows at a time go through shared memory (their
-            // 16-byte chunks XOR-swizzled so that eight rows fill the banks),
-            // so that a store covers whole sectors of several rows.
-            constexpr int CH = EC / 8;                       // chunks of a staged row
+            // 32 columns of 32 rows at a time go through shared memory (64-byte
+            // rows, their 16-byte chunks XOR-swizzled so that eight rows fill
+            // the banks), so that a store covers 64 bytes of each of eight rows.
             auto staged = [&](int row, int chunk) {
-                return stage + static_cast<uint32_t>(row * EC * 2) +
-                       ((chunk ^ ((row / (8 / CH)) % CH)) << 4);
+                return stage + static_cast<uint32_t>(row * 64) + ((chunk ^ ((row / 2) % 4)) << 4);
             };
-            unsigned short* dst[CH];                         // this lane's place in CH of the rows
+            unsigned short* dst[4];                          // this lane's place in four of the rows
 #pragma unroll
-            for (int g = 0; g < CH; ++g) {
-                const int row = (warp & 3) * 32 + g * (32 / CH) + lane / CH;
+            for (int g = 0; g < 4; ++g) {
+                const int row = (warp & 3) * 32 + g * 8 + lane / 4;
                 dst[g] = static_cast<unsigned short*>(p.o.data) +
                          (u.q0 + static_cast<int64_t>(first + (row >> gp_log2))) * p.o.row +
-                         (u.head + (row & (gp - 1))) * p.o.head + h * OW + lane % CH * 8;
+                         (u.head + (row & (gp - 1))) * p.o.head + h * OW + lane % 4 * 8;
             }
 #pragma unroll 1
             for (int c = 0; c < OW / 32; ++c) {
@@ -925,30 +908,27 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         mbar_arrive_leader<CG>(bar_output);  // O may be overwritten
                 }
                 add_zeros(ov);
+                __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 32; e += EC) {
-                    __syncwarp();
+                for (int g = 0; g < 4; ++g) {
+                    const float* f = ov + g * 8;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(staged(lane, g)),
+                                    "r"(Elem<T>::pack2(f[0] * inv, f[1] * inv)),
+                                    "r"(Elem<T>::pack2(f[2] * inv, f[3] * inv)),
+                                    "r"(Elem<T>::pack2(f[4] * inv, f[5] * inv)),
+                                    "r"(Elem<T>::pack2(f[6] * inv, f[7] * inv)) : "memory");
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int g = 0; g < CH; ++g) {
-                        const float* f = ov + e + g * 8;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     :: "r"(staged(lane, g)),
-                                        "r"(Elem<T>::pack2(f[0] * inv, f[1] * inv)),
-                                        "r"(Elem<T>::pack2(f[2] * inv, f[3] * inv)),
-                                        "r"(Elem<T>::pack2(f[4] * inv, f[5] * inv)),
-                                        "r"(Elem<T>::pack2(f[6] * inv, f[7] * inv)) : "memory");
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int g = 0; g < CH; ++g) {
-                        const int q = g * (32 / CH) + lane / CH;
-                        uint4 w;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(staged(q, lane % CH)) : "memory");
-                        if (rows >> q & 1)
-                            *reinterpret_cast<uint4*>(dst[g] + c * 32 + e) = w;
-                    }
+                for (int g = 0; g < 4; ++g) {
+                    const int q = g * 8 + lane / 4;
+                    uint4 w;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                 : "r"(staged(q, lane % 4)) : "memory");
+                    if (rows >> q & 1)
+                        *reinterpret_cast<uint4*>(dst[g] + c * 32) = w;
                 }
             }
             if (!in_place)
@@ -1052,7 +1032,7 @@ cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(units * S::CG), 1, 1);
-    cfg.blockDim = dim3(packed_threads<D>(), 1, 1);
+    cfg.blockDim = dim3(kPackedThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(packed_smem<D>());
     cfg.stream = s;
     cfg.attrs = attr;

@@ -42,26 +42,6 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t addr)
     return r;
 }
 
-// mbar_wait_bounded for waits on the critical path: plain tries, the clock read
-// once in 256 of them.
-__device__ __forceinline__ bool mbar_wait_hot(uint32_t bar, uint32_t parity)
-{
-    unsigned long long t0 = 0;
-#pragma unroll 1
-    for (uint32_t it = 1; it < (1u << 30); ++it) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((it & 255u) == 0) {
-            const unsigned long long now = global_ns();
-            if (t0 == 0)
-                t0 = now;
-            else if (now - t0 > kWaitLimitNs)
-                return false;
-        }
-    }
-    return false;
-}
-
 // Arrive on the even CTA's barrier.  What it announces lies in tensor memory
 // and is ordered by tcgen05.wait and tcgen05.fence before it; no other memory
 // is handed over, so the arrival and the waits keep the CTA scope (with

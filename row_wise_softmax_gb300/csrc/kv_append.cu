@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kThreads)
 kv_append_kernel(const AppendProblem p)
 {
     constexpr int U = D / 16;
+    constexpr int kBatch = TT == 1 ? 1 : 2;        // units that a thread has under way
     __shared__ float2 turn[TT][kMaxHalf];
     __shared__ int64_t k_at[TT], v_at[TT];         // cache element of the token, < 0: none
     __shared__ int32_t pos_of[TT];
@@ -107,68 +108,87 @@ kv_append_kernel(const AppendProblem p)
     __syncthreads();
 
     const int nq = p.q.data ? p.n_heads : 0, nk = p.cache.n_kv_heads;
-    const int per_token = (nq + 2 * nk) * U;
-    for (int i = tid; i < per_token * tokens; i += kThreads) {
-        const int t = i / per_token, r = (i - t * per_token) / U, u = i % U;
-        if (pos_of[t] < 0)
-            continue;
-        // Which tensor this head row belongs to.
-        const int64_t token = t0 + t;
-        const unsigned short* src;
-        unsigned short* dst;
-        if (r < nq) {
-            src = static_cast<const unsigned short*>(p.q.data) + token * p.q.row + r * p.q.head;
-            dst = static_cast<unsigned short*>(p.q_out.data) + token * p.q_out.row +
-                  r * p.q_out.head;
-        } else if (r < nq + nk) {
-            if (k_at[t] < 0)
-                continue;
-            src = static_cast<const unsigned short*>(p.k.data) + token * p.k.row +
-                  (r - nq) * p.k.head;
-            dst = static_cast<unsigned short*>(p.cache.k) + k_at[t] + (r - nq) * p.cache.k_head;
-        } else {
-            if (v_at[t] < 0)
-                continue;
-            src = static_cast<const unsigned short*>(p.v.data) + token * p.v.row +
-                  (r - nq - nk) * p.v.head;
-            dst = static_cast<unsigned short*>(p.cache.v) + v_at[t] +
-                  (r - nq - nk) * p.cache.v_head;
-        }
-        const bool turns = r < nq + nk && u * 16 < p.rot_dim;
-        const bool apart = turns && !p.interleaved;
-        const int c0 = apart ? u : 2 * u, c1 = apart ? u + p.rot_dim / 16 : 2 * u + 1;
-        uint4 w0 = *reinterpret_cast<const uint4*>(src + c0 * 8);
-        uint4 w1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
-        if (turns) {
-            float x[8], y[8];
-            unpack8<T>(w0, x);
-            unpack8<T>(w1, y);
-            const float2* cs = &turn[t][u * 8];
-            if (p.interleaved) {
+    const int per_token = (nq + 2 * nk) * U, units = per_token * tokens;
+    // kBatch units at a time: all of their loads are under way before the
+    // first is used.
+    for (int i0 = tid; i0 < units; i0 += kThreads * kBatch) {
+        unsigned short* dst[kBatch];               // null: nothing to do
+        uint4 w0[kBatch], w1[kBatch];
+        int c0[kBatch], c1[kBatch], turn_at[kBatch];   // turn_at < 0: copied as it is
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 a = cs[j], b = cs[j + 4];
-                    const float x0 = x[2 * j], x1 = x[2 * j + 1];
-                    const float y0 = y[2 * j], y1 = y[2 * j + 1];
-                    x[2 * j] = x0 * a.x - x1 * a.y;
-                    x[2 * j + 1] = x0 * a.y + x1 * a.x;
-                    y[2 * j] = y0 * b.x - y1 * b.y;
-                    y[2 * j + 1] = y0 * b.y + y1 * b.x;
-                }
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            dst[b] = nullptr;
+            if (i >= units)
+                continue;
+            const int t = TT == 1 ? 0 : i / per_token, r = (i - t * per_token) / U, u = i % U;
+            if (pos_of[t] < 0)
+                continue;
+            // Which tensor this head row belongs to.
+            const int64_t token = t0 + t;
+            const unsigned short* src;
+            if (r < nq) {
+                src = static_cast<const unsigned short*>(p.q.data) + token * p.q.row + r * p.q.head;
+                dst[b] = static_cast<unsigned short*>(p.q_out.data) + token * p.q_out.row +
+                         r * p.q_out.head;
+            } else if (r < nq + nk) {
+                if (k_at[t] < 0)
+                    continue;
+                src = static_cast<const unsigned short*>(p.k.data) + token * p.k.row +
+                      (r - nq) * p.k.head;
+                dst[b] = static_cast<unsigned short*>(p.cache.k) + k_at[t] +
+                         (r - nq) * p.cache.k_head;
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 a = cs[j];
-                    const float x0 = x[j], y0 = y[j];
-                    x[j] = x0 * a.x - y0 * a.y;
-                    y[j] = x0 * a.y + y0 * a.x;
-                }
+                if (v_at[t] < 0)
+                    continue;
+                src = static_cast<const unsigned short*>(p.v.data) + token * p.v.row +
+                      (r - nq - nk) * p.v.head;
+                dst[b] = static_cast<unsigned short*>(p.cache.v) + v_at[t] +
+                         (r - nq - nk) * p.cache.v_head;
             }
-            w0 = pack8<T>(x);
-            w1 = pack8<T>(y);
+            const bool turns = r < nq + nk && u * 16 < p.rot_dim;
+            const bool apart = turns && !p.interleaved;
+            turn_at[b] = turns ? t * kMaxHalf + u * 8 : -1;
+            c0[b] = apart ? u : 2 * u;
+            c1[b] = apart ? u + p.rot_dim / 16 : 2 * u + 1;
+            w0[b] = *reinterpret_cast<const uint4*>(src + c0[b] * 8);
+            w1[b] = *reinterpret_cast<const uint4*>(src + c1[b] * 8);
         }
-        *reinterpret_cast<uint4*>(dst + c0 * 8) = w0;
-        *reinterpret_cast<uint4*>(dst + c1 * 8) = w1;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (!dst[b])
+                continue;
+            if (turn_at[b] >= 0) {
+                float x[8], y[8];
+                unpack8<T>(w0[b], x);
+                unpack8<T>(w1[b], y);
+                const float2* cs = &turn[0][0] + turn_at[b];
+                if (p.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = cs[j], g = cs[j + 4];
+                        const float x0 = x[2 * j], x1 = x[2 * j + 1];
+                        const float y0 = y[2 * j], y1 = y[2 * j + 1];
+                        x[2 * j] = x0 * f.x - x1 * f.y;
+                        x[2 * j + 1] = x0 * f.y + x1 * f.x;
+                        y[2 * j] = y0 * g.x - y1 * g.y;
+                        y[2 * j + 1] = y0 * g.y + y1 * g.x;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = cs[j];
+                        const float x0 = x[j], y0 = y[j];
+                        x[j] = x0 * f.x - y0 * f.y;
+                        y[j] = x0 * f.y + y0 * f.x;
+                    }
+                }
+                w0[b] = pack8<T>(x);
+                w1[b] = pack8<T>(y);
+            }
+            *reinterpret_cast<uint4*>(dst[b] + c0[b] * 8) = w0[b];
+            *reinterpret_cast<uint4*>(dst[b] + c1[b] * 8) = w1[b];
+        }
     }
 }
 
