@@ -201,55 +201,62 @@ __device__ __forceinline__ int32_t units_with(int32_t n_q, int32_t n_k, int tok_
 
 // Finds unit number `rank` in the order in which units are handed out, by a
 // warp: the units that visit most key tiles first, so that the ones dispatched
-// last are short.  The sequences' bounds are read once and kept, four to a
-// lane; above kRanked sequences the order is that of the sequences instead,
-// and the walk goes on from where the last one ended.
+// last are short.  The sequences' bounds are read once and kept in shared
+// memory (in registers they made the copy warp spill); above kRanked sequences
+// the order is that of the sequences instead, and the walk goes on from where
+// the last one ended.
 constexpr int kRanked = 128;
+
+struct Bounds {
+    int32_t q0[kRanked], n_q[kRanked], k0[kRanked], n_k[kRanked];
+};
 
 template <int BN>
 struct UnitFinder {
-    int32_t q0[4], n_q[4], k0[4], n_k[4];
+    Bounds* b;
     int32_t most;                                  // most key tiles of a unit
     int64_t total;                                 // units (ranked), or past the end
     int64_t at, before;                            // unranked: sequence block, units before it
 
+    // Bounds of sequence s into place i (of this lane).
     __device__ __forceinline__ void lengths(const PackedProblem& p, int64_t s, int i, bool report)
     {
-        int64_t a = 0, b = 0, c = 0, d = 0;
-        if (s < p.n_seqs && !sequence_of(p, s, a, b, c, d) && report)
+        int64_t q = 0, nq = 0, k = 0, nk = 0;
+        if (s < p.n_seqs && !sequence_of(p, s, q, nq, k, nk) && report)
             atomicOr(&g_error_attention_packed, kErrBadIndex);
-        q0[i] = static_cast<int32_t>(a);
-        n_q[i] = static_cast<int32_t>(b);
-        k0[i] = static_cast<int32_t>(c);
-        n_k[i] = static_cast<int32_t>(d);
+        b->q0[i] = static_cast<int32_t>(q);
+        b->n_q[i] = static_cast<int32_t>(nq);
+        b->k0[i] = static_cast<int32_t>(k);
+        b->n_k[i] = static_cast<int32_t>(nk);
     }
 
     // Units that visit at least x key tiles.
     __device__ __forceinline__ int32_t count(const PackedProblem& p, int tok_log2, int32_t x) const
     {
         int32_t n = 0, first;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            n += units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, x, first);
+        for (int i = threadIdx.x & 31; i < p.n_seqs; i += 32)
+            n += units_with<BN>(b->n_q[i], b->n_k[i], tok_log2, p.causal, x, first);
         return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
     }
 
-    __device__ void init(const PackedProblem& p, int tok_log2, bool report)
+    __device__ void init(const PackedProblem& p, Bounds* bounds, int tok_log2, bool report)
     {
         const int lane = threadIdx.x & 31;
+        b = bounds;
         at = before = 0;
         total = INT64_MAX;
         if (p.n_seqs > kRanked) {
             for (int64_t s = lane; report && s < p.n_seqs; s += 32)
-                lengths(p, s, 0, true);
+                lengths(p, s, lane, true);
             return;
         }
         int32_t longest = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lengths(p, i * 32 + lane, i, report);
-            longest = n_q[i] > 0 ? max(longest, static_cast<int32_t>((n_k[i] + BN - 1u) / BN)) : longest;
+        for (int i = lane; i < kRanked; i += 32) {
+            lengths(p, i, i, report);
+            if (b->n_q[i] > 0)
+                longest = max(longest, static_cast<int32_t>((b->n_k[i] + BN - 1u) / BN));
         }
+        __syncwarp();
         most = __reduce_max_sync(0xffffffffu, longest);
         total = count(p, tok_log2, 0);
     }
@@ -277,17 +284,9 @@ struct UnitFinder {
         return lane_of;
     }
 
-    __device__ __forceinline__ Unit unit(int i, int lane_of, int32_t tile) const
+    __device__ __forceinline__ Unit unit(int i, int32_t tile) const
     {
-        Unit u;
-        u.q0 = __shfl_sync(0xffffffffu, q0[i], lane_of);
-        u.n_q = __shfl_sync(0xffffffffu, n_q[i], lane_of);
-        u.k0 = __shfl_sync(0xffffffffu, k0[i], lane_of);
-        u.n_k = __shfl_sync(0xffffffffu, n_k[i], lane_of);
-        u.tile = tile;
-        u.head = 0;
-        u.ok = 1;
-        return u;
+        return Unit{b->q0[i], b->n_q[i], b->k0[i], b->n_k[i], tile, 0, 1};
     }
 
     __device__ Unit find(const PackedProblem& p, int64_t rank, int tok_log2)
@@ -301,14 +300,16 @@ struct UnitFinder {
             if (rank < before)
                 at = before = 0;
             for (; at < p.n_seqs; at += 32) {
-                lengths(p, at + lane, 0, false);
+                __syncwarp();
+                lengths(p, at + lane, lane, false);
+                __syncwarp();
                 int64_t left = rank - before;
                 int32_t first;
-                const int32_t n = units_with<BN>(n_q[0], n_k[0], tok_log2, p.causal, 0, first);
+                const int32_t n =
+                    units_with<BN>(b->n_q[lane], b->n_k[lane], tok_log2, p.causal, 0, first);
                 const int l = pick(n, left, passed);
                 if (l >= 0)                        // longest first within the sequence
-                    return unit(0, l, __shfl_sync(0xffffffffu, n, l) - 1 -
-                                          static_cast<int32_t>(left));
+                    return unit(l, __shfl_sync(0xffffffffu, n, l) - 1 - static_cast<int32_t>(left));
                 before += passed;
             }
             total = rank;
@@ -326,14 +327,14 @@ struct UnitFinder {
             }
         }
         int64_t left = rank - above;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = lane; i - lane < p.n_seqs; i += 32) {
             int32_t first, next;
-            int32_t n = units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, lo, first);
-            n -= units_with<BN>(n_q[i], n_k[i], tok_log2, p.causal, lo + 1, next);
+            int32_t n = units_with<BN>(b->n_q[i], b->n_k[i], tok_log2, p.causal, lo, first);
+            n -= units_with<BN>(b->n_q[i], b->n_k[i], tok_log2, p.causal, lo + 1, next);
             const int l = pick(n, left, passed);
             if (l >= 0)
-                return unit(i, l, __shfl_sync(0xffffffffu, first, l) + static_cast<int32_t>(left));
+                return unit(i - lane + l,
+                            __shfl_sync(0xffffffffu, first, l) + static_cast<int32_t>(left));
         }
         return none;
     }
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ CUtensorMap map_o,
                         const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2)
 {
     using S = Shape<D>;
@@ -373,6 +375,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     __shared__ __align__(8) unsigned long long next_full[2], next_free[2];
     __shared__ __align__(16) uint4 s_next[2];                // answers of cluster launch control
     __shared__ Unit s_unit[2];
+    __shared__ Bounds s_bounds;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_failed;
     __shared__ int s_stop[2][2];
@@ -465,7 +468,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         const int tok_log2 = 8 + (CG - 1) - gp_log2;
         const uint32_t blocks = static_cast<uint32_t>(p.n_heads) >> gp_log2;
         UnitFinder<BN> finder;
-        finder.init(p, tok_log2, blockIdx.x == 0);
+        finder.init(p, &s_bounds, tok_log2, blockIdx.x == 0);
         auto find = [&](uint32_t cta) {
             const uint32_t index = cta / CG, unit = index / blocks;
             Unit u = finder.find(p, unit, tok_log2);
@@ -883,19 +886,14 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             // A row that sees no key is the softmax of only -inf: NaN.
             const float inv = limit > 0 ? 1.0f / l : __int_as_float(0x7fc00000);
             // 32 columns of 32 rows at a time go through shared memory (64-byte
-            // rows, their 16-byte chunks XOR-swizzled so that eight rows fill
-            // the banks), so that a store covers 64 bytes of each of eight rows.
+            // rows in the copy engine's 64-byte swizzle: 16-byte chunks XORed
+            // by row pair).  When every row is stored, one tensor-map copy
+            // takes them from there and the warp goes on; else each row of 64
+            // bytes is stored by four lanes.
             auto staged = [&](int row, int chunk) {
                 return stage + static_cast<uint32_t>(row * 64) + ((chunk ^ ((row / 2) % 4)) << 4);
             };
-            unsigned short* dst[4];                          // this lane's place in four of the rows
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int row = (warp & 3) * 32 + g * 8 + lane / 4;
-                dst[g] = static_cast<unsigned short*>(p.o.data) +
-                         (u.q0 + static_cast<int64_t>(first + (row >> gp_log2))) * p.o.row +
-                         (u.head + (row & (gp - 1))) * p.o.head + h * OW + lane % 4 * 8;
-            }
+            const bool all_rows = rows == 0xffffffffu;
 #pragma unroll 1
             for (int c = 0; c < OW / 32; ++c) {
                 float ov[32];
@@ -908,6 +906,8 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         mbar_arrive_leader<CG>(bar_output);  // O may be overwritten
                 }
                 add_zeros(ov);
+                if (lane == 0)                               // the copy before has read its rows
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -919,20 +919,42 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                                     "r"(Elem<T>::pack2(f[4] * inv, f[5] * inv)),
                                     "r"(Elem<T>::pack2(f[6] * inv, f[7] * inv)) : "memory");
                 }
-                __syncwarp();
+                if (all_rows) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile(
+                            "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
+                            " [%0, {%1, %2, %3}], [%4];\n\tcp.async.bulk.commit_group;"
+                            :: "l"(reinterpret_cast<uint64_t>(&map_o)), "r"(h * OW + c * 32),
+                               "r"(u.head), "r"(u.q0 + first + ((warp & 3) * 32 >> gp_log2)),
+                               "r"(stage) : "memory");
+                } else {
+                    __syncwarp();
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int q = g * 8 + lane / 4;
-                    uint4 w;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                 : "r"(staged(q, lane % 4)) : "memory");
-                    if (rows >> q & 1)
-                        *reinterpret_cast<uint4*>(dst[g] + c * 32) = w;
+                    for (int g = 0; g < 4; ++g) {
+                        const int q = g * 8 + lane / 4, row = (warp & 3) * 32 + q;
+                        uint4 w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(staged(q, lane % 4)) : "memory");
+                        if (rows >> q & 1)
+                            *reinterpret_cast<uint4*>(
+                                static_cast<unsigned short*>(p.o.data) +
+                                (u.q0 + static_cast<int64_t>(first + (row >> gp_log2))) * p.o.row +
+                                (u.head + (row & (gp - 1))) * p.o.head + h * OW + c * 32 +
+                                lane % 4 * 8) = w;
+                    }
                 }
             }
-            if (!in_place)
+            if (!in_place) {
                 redo = leaked(not_finite());
+                if (redo) {                                  // after the copies that are under way
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    named_barrier(pair_bar, 32 * HS);
+                }
+            }
             if (p.lse && h == 0 && (rows >> lane & 1))
                 p.lse[(u.q0 + static_cast<int64_t>(token)) * p.n_heads + u.head + (r & (gp - 1))] =
                     limit > 0 && l != 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : kNegInf;
@@ -945,6 +967,8 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                                        CAUSAL ? min(u.n_k, tok + off + 1) : u.n_k, scale_log2);
             }
         }
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -970,10 +994,10 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
 }
 
 // 3-D tensor map (element, head, row) of a [rows][heads][D] operand: boxes of
-// 64 elements (128 bytes, 128-byte swizzle) x box_heads x box_rows; rows past
-// the tensor's end read as zero.
+// 64 elements (128 bytes, 128-byte swizzle) x box_heads x box_rows, or of 32
+// (64 bytes, 64-byte swizzle); rows past the tensor's end read as zero.
 inline bool packed_tensor_map(CUtensorMap* map, const Heads& t, int64_t rows, int64_t heads, int d,
-                              int box_heads, int box_rows, int dtype)
+                              int box_heads, int box_rows, int dtype, int box_elems = 64)
 {
     auto encode = tensor_map_encoder();
     if (!encode)
@@ -987,13 +1011,13 @@ inline bool packed_tensor_map(CUtensorMap* map, const Heads& t, int64_t rows, in
                                 static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2,
                                    static_cast<cuuint64_t>(rs) * 2};
-    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_elems), static_cast<cuuint32_t>(box_heads),
                                static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estride[3] = {1u, 1u, 1u};
     return encode(map, dtype == SOFTMAX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   3, t.data, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  box_elems == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1011,11 +1035,13 @@ cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
     const int64_t units = (p.total_q / tokens + p.n_seqs) * (p.n_heads >> gp_log2);
     if (units * S::CG > 0x7fffffff)
         return cudaErrorNotSupported;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (p.total_k == 0 ||
         !packed_tensor_map(&mq, p.q, p.total_q, p.n_heads, D, 1 << gp_log2, tile_tokens, p.dtype) ||
         !packed_tensor_map(&mk, p.k, p.total_k, p.n_kv_heads, D, 1, S::BN / S::CG, p.dtype) ||
-        !packed_tensor_map(&mv, p.v, p.total_k, p.n_kv_heads, D, 1, S::BN, p.dtype))
+        !packed_tensor_map(&mv, p.v, p.total_k, p.n_kv_heads, D, 1, S::BN, p.dtype) ||
+        !packed_tensor_map(&mo, p.o, p.total_q, p.n_heads, D, 1 << gp_log2, 32 >> gp_log2, p.dtype,
+                           32))
         return cudaErrorNotSupported;                    // nothing launched
     auto* kern = attention_packed_kernel<T, D, CAUSAL>;
     static std::atomic<bool> attr_set[64];
@@ -1038,7 +1064,7 @@ cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, S::CG));
     const float scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p, scale_log2, gp_log2);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p, scale_log2, gp_log2);
     note_launch();
     return err;
 }
