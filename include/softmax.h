@@ -272,7 +272,7 @@ typedef struct {
  * t mod page_size.  k and v may be parts of one allocation; each token's
  * heads must have places of their own.  n_pages: entries of the table
  * outside [0, n_pages) are bad (see above); entries of pages that a call
- * does not reach are not read.  table_width * page_size <= 2^30.
+ * does not reach are not followed.  table_width * page_size <= 2^30.
  */
 typedef struct {
     void* k;
@@ -368,7 +368,7 @@ int64_t softmax_attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int6
  *              as they were, rows in two hold either's result.
  *   A query that sees no key gives NaN (lse = -inf).  Values that a query
  *   does not see have no influence on it, whatever they hold.
- *   total_q and total_k below 2^31.
+ *   total_q and total_k are at most 2^31 - 2^16.
  */
 int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
                              const softmax_heads_t* v, const softmax_heads_t* o, float* lse,

@@ -11,6 +11,8 @@ namespace {
 constexpr int64_t kMaxCapacity = int64_t{1} << 30;
 constexpr int64_t kMaxStride = int64_t{1} << 47;          // elements: products stay in int64
 constexpr int64_t kMaxCount = int64_t{1} << 31;           // rows, heads, sequences: below
+constexpr int64_t kMaxPacked = kMaxCount - 65536;         // packed rows: a tile past the last
+                                                          // one still counts in 32 bits
 
 struct Span {                                            // bytes [a, b)
     uintptr_t a, b;
@@ -276,9 +278,9 @@ int softmax_attention_decode(const softmax_paged_cache_t* cache, const softmax_h
     const Span so = span_of(*o, b, n_heads, d), sq = span_of(*q, b, n_heads, d);
     if (meet(so, ck) || meet(so, cv))
         return SOFTMAX_ERR_INVALID_ARG;
+    const uintptr_t a_lse = reinterpret_cast<uintptr_t>(lse);
+    const Span sl{a_lse, a_lse + (lse ? static_cast<uintptr_t>(b * n_heads) * 4 : 0)};
     if (lse) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(lse);
-        const Span sl{a, a + static_cast<uintptr_t>(b * n_heads) * 4};
         if (meet(sl, so) || meet(sl, sq) || meet(sl, ck) || meet(sl, cv))
             return SOFTMAX_ERR_INVALID_ARG;
     }
@@ -291,7 +293,7 @@ int softmax_attention_decode(const softmax_paged_cache_t* cache, const softmax_h
             return SOFTMAX_ERR_INVALID_ARG;
         const uintptr_t a = reinterpret_cast<uintptr_t>(workspace);
         const Span sw{a, a + need};
-        if (meet(sw, so) || meet(sw, sq) || meet(sw, ck) || meet(sw, cv))
+        if (meet(sw, so) || meet(sw, sq) || meet(sw, sl) || meet(sw, ck) || meet(sw, cv))
             return SOFTMAX_ERR_INVALID_ARG;
     }
     p.q = heads(*q);
@@ -314,8 +316,8 @@ int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
                              int64_t n_kv_heads, int64_t head_dim, float scale, int causal,
                              int dtype, void* stream)
 {
-    if (n_seqs < 0 || n_seqs >= kMaxCount || total_q < 0 || total_q >= kMaxCount || total_k < 0 ||
-        total_k >= kMaxCount || n_heads < 1 || n_heads >= kMaxCount || n_kv_heads < 1 ||
+    if (n_seqs < 0 || n_seqs >= kMaxCount || total_q < 0 || total_q > kMaxPacked || total_k < 0 ||
+        total_k > kMaxPacked || n_heads < 1 || n_heads >= kMaxCount || n_kv_heads < 1 ||
         n_heads % n_kv_heads || !(scale > 0.0f) || !(scale <= 0x1p127f) ||
         (causal != 0 && causal != 1))
         return SOFTMAX_ERR_INVALID_ARG;

@@ -670,3 +670,28 @@ def test_binding_checks():
     rws.kv_append(s["pk"][:0], s["pv"][:0], s["kc"], s["vc"], s["table"], s["pos"][:0])
     assert rws.launch_count() == before             # nothing to do
     assert rws.device_status() == rws.OK
+
+
+def test_decode_outputs_in_the_workspace_are_refused():
+    from row_wise_softmax_gb300 import serving as sv
+    lib = sv._lib()
+    b, h, d, pages, size = 2, 4, 128, 256, 64
+    need = lib.softmax_attention_decode_workspace(b, h, 1, d, 1 << 19)
+    assert need >= 4096                               # not the form that needs none
+    kc = torch.zeros(pages, size, 1, d, device="cuda", dtype=torch.bfloat16)
+    vc, q = torch.zeros_like(kc), torch.zeros(b, h, d, device="cuda", dtype=torch.bfloat16)
+    table = torch.zeros(b, (1 << 19) // size, device="cuda", dtype=torch.int32)
+    lengths, ws = ints([5, 70]), torch.zeros(need + 1024, device="cuda", dtype=torch.uint8)
+    c = sv._cache("t", kc, vc, table, kc.shape, kc.dtype, 0)
+    x, o = sv._heads("t", "q", q, q.dtype, 0), torch.empty_like(q)
+
+    def call(out, lse):
+        return lib.softmax_attention_decode(c, x, out, lse, h, lengths.data_ptr(), 1.0, rws.BF16,
+                                            ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    y = sv._heads("t", "o", o, o.dtype, 0)
+    inside = sv._HEADS(ws.data_ptr() + 512, h * d, d)
+    assert call(y, ws.data_ptr() + 256) == rws.ERR_INVALID_ARG
+    assert call(inside, None) == rws.ERR_INVALID_ARG
+    assert call(y, ws.data_ptr() + need) == rws.OK    # just behind it
+    torch.cuda.synchronize()
+    assert torch.equal(o, torch.zeros_like(o))

@@ -122,6 +122,16 @@ def test_packed_refusals(lib):
                   o=heads(MB + 1024, row)) == bad
 
 
+@no_gpu
+@pytest.mark.parametrize("key", ["tq", "tk"])
+def test_packed_rows_that_a_tile_could_pass(lib, key):
+    """A tile that begins at the last row ends past it, still below 2^31."""
+    most = (1 << 31) - (1 << 16)
+    far = dict(q=heads(1 << 50), o=heads(1 << 54), k=heads(1 << 56), v=heads(1 << 57))
+    assert packed(lib, **far, **{key: most}) == good()
+    assert packed(lib, **far, **{key: most + 1}) == rws.ERR_INVALID_ARG
+
+
 def append(lib, c=None, k=None, v=None, q=None, o=None, h=4, pos=32 * MB, ids=33 * MB, n=5,
            freq=34 * MB, rot=128, inter=0, dtype=rws.F16):
     return lib.softmax_kv_append(
