@@ -104,6 +104,21 @@ def _cache(name, k, v, table, shape, dtype, device):
 _current = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
+# A contiguous tensor on the current device.  torch's allocation without its
+# dispatcher, where torch offers that: between two kernel launches
+# torch.empty_like costs 4.7 us of host time, this 1.4 (attention_decode of 8
+# sequences: 13.1 us of host time a call, then 10.4).
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _empty3(shape, dtype):
+    a, b, c = shape
+    return _empty_strided_cuda((a, b, c), (b * c, c, 1), dtype)
+
 
 def _elsewhere(name, device, stream, call):
     """call() with CUDA device ``device`` and ``stream`` (a torch stream, a raw
@@ -186,7 +201,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=Non
             raise ValueError("kv_append: q must be [tokens, heads, head_dim]")
         h = shape[1]
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _empty3(shape, dtype)
         elif q_out.shape != shape:
             raise ValueError("kv_append: q_out must match q")
         qs = _heads(name, "q", q, dtype, device)
@@ -236,12 +251,12 @@ def attention_decode(q, k_cache, v_cache, page_table, lengths, scale: float | No
         raise ValueError("attention_decode: page_table must have a row for each query")
     lens = _index(name, "lengths", lengths, b, device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty3(qshape, dtype)
     elif out.shape != qshape:
         raise ValueError("attention_decode: out must match q")
-    lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = _empty_strided_cuda((b, h), (h, 1), torch.float32) if return_lse else None
     need = _decode_workspace(device, b, h, hk, d, width * size)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    ws = _empty_strided_cuda((need,), (1,), torch.uint8) if need > 0 else None
     st = (_declared or _lib()).softmax_attention_decode(
         cache, _heads(name, "q", q, dtype, device), _heads(name, "out", out, dtype, device),
         lse.data_ptr() if return_lse else None, h, lens, d ** -0.5 if scale is None else scale,
@@ -289,10 +304,10 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     cq = _index(name, "cu_q", cu_q, seqs + 1, device)
     ck = cq if cu_k is None else _index(name, "cu_k", cu_k, seqs + 1, device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty3(qshape, dtype)
     elif out.shape != qshape:
         raise ValueError("attention_packed: out must match q")
-    lse = torch.empty((n, h), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = _empty_strided_cuda((n, h), (h, 1), torch.float32) if return_lse else None
     st = (_declared or _lib()).softmax_attention_packed(
         _heads(name, "q", q, dtype, device), _heads(name, "k", k, dtype, device),
         _heads(name, "v", v, dtype, device), _heads(name, "out", out, dtype, device),
