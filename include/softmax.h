@@ -369,13 +369,22 @@ int64_t softmax_attention_decode_workspace(int64_t n_seqs, int64_t n_heads, int6
  *   A query that sees no key gives NaN (lse = -inf).  Values that a query
  *   does not see have no influence on it, whatever they hold.
  *   total_q and total_k are at most 2^31 - 2^16.
+ *   workspace  as for softmax_attention_decode, of at least
+ *              softmax_attention_packed_workspace bytes.
  */
 int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
                              const softmax_heads_t* v, const softmax_heads_t* o, float* lse,
                              const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
                              int64_t total_q, int64_t total_k, int64_t n_heads,
                              int64_t n_kv_heads, int64_t head_dim, float scale, int causal,
-                             int dtype, void* stream);
+                             int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that softmax_attention_packed needs on the current
+ * device for these sizes (calls of few query rows over long sequences do);
+ * 0 is a valid answer, -1 says that a size is invalid or that there is no
+ * usable device. */
+int64_t softmax_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k,
+                                           int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
 
 /*
  * softmax_strided: the softmax of rows whose elements are not contiguous.

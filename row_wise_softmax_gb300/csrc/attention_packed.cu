@@ -158,6 +158,8 @@ constexpr int kHS = 2;                             // warps that share a row of 
 constexpr int kSoftWarps = 2 * 4 * kHS;            // two query tiles of four TMEM lane groups
 constexpr int kStageBytes = 32 * 64;               // a warp's place for 32 x 32 outputs
 
+constexpr int kPartTiles = 2;                      // key tiles of a part, at least
+
 constexpr int kPackedThreads = (kSoftWarps + 3) * 32;    // softmax, two MMA warps, copy
 
 template <int D>
@@ -173,6 +175,20 @@ struct Unit {
     int32_t q0, n_q, k0, n_k;
     int32_t tile, head;                            // head: first of the block
     int32_t ok;
+    int32_t lo, hi, slot;                          // kParts: its key tiles, its place for the sum
+};
+
+// What the kernel does with a unit: all of its keys, all of them with the
+// causal mask, or (either mask) one of the equal parts that its key tiles are
+// cut into, whose unnormalised sum goes to the workspace for the join kernel.
+enum : int { kFull = 0, kCausal = 1, kParts = 2 };
+
+// A part's sum over a query tile, in the workspace: O as [D / 4][128 rows] of
+// four columns (a warp's rows side by side), then (m, l) of each row.
+template <int D>
+struct PartSum {
+    float4 o[D / 4][kBM];
+    float2 ml[kBM];
 };
 
 // Number of a sequence's units (of 2^tok_log2 query tokens) that visit at least
@@ -214,6 +230,7 @@ struct Bounds {
 template <int BN>
 struct UnitFinder {
     Bounds* b;
+    bool ranked;
     int32_t most;                                  // most key tiles of a unit
     int64_t total;                                 // units (ranked), or past the end
     int64_t at, before;                            // unranked: sequence block, units before it
@@ -239,13 +256,15 @@ struct UnitFinder {
         return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
     }
 
-    __device__ void init(const PackedProblem& p, Bounds* bounds, int tok_log2, bool report)
+    __device__ void init(const PackedProblem& p, Bounds* bounds, int tok_log2, bool report,
+                         bool by_length)
     {
         const int lane = threadIdx.x & 31;
         b = bounds;
+        ranked = by_length && p.n_seqs <= kRanked;
         at = before = 0;
         total = INT64_MAX;
-        if (p.n_seqs > kRanked) {
+        if (!ranked) {
             for (int64_t s = lane; report && s < p.n_seqs; s += 32)
                 lengths(p, s, lane, true);
             return;
@@ -296,7 +315,7 @@ struct UnitFinder {
         if (rank >= total)
             return none;
         int64_t passed;
-        if (p.n_seqs > kRanked) {
+        if (!ranked) {
             if (rank < before)
                 at = before = 0;
             for (; at < p.n_seqs; at += 32) {
@@ -340,15 +359,17 @@ struct UnitFinder {
     }
 };
 
-template <typename T, int D, bool CAUSAL>
+template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kPackedThreads, 1)
 attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CUtensorMap map_o,
-                        const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2)
+                        const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2,
+                        int n_parts)
 {
     using S = Shape<D>;
+    const bool causal = MODE == kParts ? p.causal != 0 : MODE == kCausal;
     constexpr int CG = S::CG, BN = S::BN, KVS = S::KVS, HS = kHS;
     constexpr bool kBF16 = Elem<T>::kNegInfBits == 0xff80u;
     constexpr uint32_t QT_BYTES = kBM * D * 2;               // a query tile
@@ -443,15 +464,22 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     };
     // Key tiles that query tile x of a unit visits (both CTAs' parts of it),
     // -1 when it has no tokens at all.
-    auto tiles_of = [&](const Unit& u, int x) -> int32_t {
+    auto all_tiles_of = [&](const Unit& u, int x) -> int32_t {
         const int32_t begin = u.tile * tokens + x * CG * tile_tokens;
         if (u.ok <= 0 || begin >= u.n_q)
             return -1;
         int32_t lim = u.n_k;
-        if (CAUSAL)
+        if (causal)
             lim = min(lim, min(begin + CG * tile_tokens, u.n_q) + u.n_k - u.n_q);
         return lim <= 0 ? 0 : (lim + BN - 1) / BN;
     };
+    // Those that it visits here: all of them, or those of the unit's part.
+    auto tiles_of = [&](const Unit& u, int x) -> int32_t {
+        const int32_t n = all_tiles_of(u, x);
+        return MODE != kParts || n <= 0 ? n : max(min(n, u.hi) - u.lo, 0);
+    };
+    // First key row of the first of them.
+    auto key0_of = [&](const Unit& u) { return MODE == kParts ? u.k0 + u.lo * BN : u.k0; };
     // Tile number t, counted through all units, lies in ring slot t % KVS.
     auto slot = [](uint32_t t) { return t % KVS; };
     auto phase = [](uint32_t t) { return (t / KVS) & 1u; };
@@ -468,11 +496,19 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         const int tok_log2 = 8 + (CG - 1) - gp_log2;
         const uint32_t blocks = static_cast<uint32_t>(p.n_heads) >> gp_log2;
         UnitFinder<BN> finder;
-        finder.init(p, &s_bounds, tok_log2, blockIdx.x == 0);
+        finder.init(p, &s_bounds, tok_log2, blockIdx.x == 0, MODE != kParts);
         auto find = [&](uint32_t cta) {
-            const uint32_t index = cta / CG, unit = index / blocks;
+            const uint32_t slot = cta / CG, index = MODE == kParts ? slot / n_parts : slot;
+            const uint32_t unit = index / blocks;
             Unit u = finder.find(p, unit, tok_log2);
             u.head = static_cast<int32_t>((index - unit * blocks) << gp_log2);
+            if constexpr (MODE == kParts) {
+                const int64_t n = max(0, max(all_tiles_of(u, 0), all_tiles_of(u, 1)));
+                const int64_t part = slot - index * n_parts;
+                u.lo = static_cast<int32_t>(n * part / n_parts);
+                u.hi = static_cast<int32_t>(n * (part + 1) / n_parts);
+                u.slot = static_cast<int32_t>(slot);
+            }
             return u;
         };
         uint32_t kv = 0, q_uses = 0;
@@ -528,7 +564,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
                             tma_load_3d<CG>(sK + slot(kv) * KV_BYTES + c * (KR * 128), &map_k,
-                                            c * 64, kvh, u.k0 + t * BN +
+                                            c * 64, kvh, key0_of(u) + t * BN +
                                             static_cast<int>(rank) * KR, bar_k);
                     }
                     if (kv >= KVS)
@@ -536,7 +572,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                     const uint32_t bar_v = announce(&v_full[slot(kv)], KV_BYTES);
                     if (one && !failed)
                         tma_load_3d<CG>(sV + slot(kv) * KV_BYTES, &map_v,
-                                        static_cast<int>(rank) * VD, kvh, u.k0 + t * BN, bar_v);
+                                        static_cast<int>(rank) * VD, kvh, key0_of(u) + t * BN, bar_v);
                     ++kv;
                 }
                 // The answer (both CTAs get the same), and which unit that
@@ -726,9 +762,11 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             const int32_t off = u.n_k - u.n_q;
             const int32_t first = u.tile * tokens + (x * CG + static_cast<int>(rank)) * tile_tokens;
             const int32_t token = first + (r >> gp_log2);    // of the sequence
-            // Keys visible to this row, and to every row of the tile.
-            const int32_t limit = CAUSAL ? min(u.n_k, token + off + 1) : u.n_k;
-            const int32_t limit_all = CAUSAL ? min(u.n_k, first + off + 1) : u.n_k;
+            // Keys visible to this row, and to every row of the tile (counted
+            // from the first of the part).
+            const int32_t skipped = MODE == kParts ? u.lo * BN : 0;
+            const int32_t limit = (causal ? min(u.n_k, token + off + 1) : u.n_k) - skipped;
+            const int32_t limit_all = (causal ? min(u.n_k, first + off + 1) : u.n_k) - skipped;
             float m = kNegInf, l = 0.0f;                     // l: this warp's part of the sum
             for (int32_t t = 0; t < my_kt; ++t) {
                 await(1 + x, &bar_s[x], done + static_cast<uint32_t>(t), true);
@@ -823,7 +861,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             // such a value in the masked part of their key tiles, are done
             // again over their visible keys alone, after the others have been
             // stored; where o is q, nothing may be stored in them before.
-            const bool in_place = p.o.data == p.q.data;
+            const bool in_place = MODE != kParts && p.o.data == p.q.data;
             float zero0 = 0.0f, zero1 = 0.0f;                // 0 * O: NaN unless O is finite
             auto add_zeros = [&](const float (&v)[32]) {
 #pragma unroll
@@ -859,11 +897,12 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             auto leaked = [&](unsigned redo) {
                 if (redo) {
                     const unsigned short* const v = static_cast<const unsigned short*>(p.v.data) +
-                                                    static_cast<int64_t>(u.k0) * p.v.row +
+                                                    static_cast<int64_t>(key0_of(u)) * p.v.row +
                                                     kvh * p.v.head;
                     const int32_t from = __reduce_min_sync(0xffffffffu,
                                                            redo >> lane & 1 ? limit : 0x7fffffff);
-                    const int64_t to = min(static_cast<int64_t>(my_kt) * BN, p.total_k - u.k0);
+                    const int64_t to =
+                        min(static_cast<int64_t>(my_kt) * BN, p.total_k - key0_of(u));
                     bool hit = false;
                     for (int64_t e = static_cast<int64_t>(from) * (D / 2) + lane; e < to * (D / 2);
                          e += 32) {
@@ -879,6 +918,61 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 return redo;
             };
             unsigned redo = 0;
+            if constexpr (MODE == kParts) {
+                // The sum as it is; a row that has to be done again over what
+                // it sees of the part replaces its own.
+                auto* const sum = static_cast<PartSum<D>*>(p.workspace) +
+                                  (static_cast<int64_t>(u.slot) * 2 + x) * CG + rank;
+#pragma unroll 1
+                for (int c = 0; c < OW / 32; ++c) {
+                    float ov[32];
+                    tmem_ld32(t_row + o_col + c * 32, ov);
+                    tmem_wait_ld();
+                    add_zeros(ov);
+                    if (!broken)
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            sum->o[(h * OW + c * 32) / 4 + g][r] =
+                                make_float4(ov[4 * g], ov[4 * g + 1], ov[4 * g + 2], ov[4 * g + 3]);
+                }
+                if (my_kt > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_leader<CG>(bar_output);  // O may be overwritten
+                }
+                if (h == 0 && !broken)
+                    sum->ml[r] = make_float2(m, l);          // (-inf, 0): nothing was seen
+                redo = not_finite();
+                redo = my_kt > 0 ? leaked(redo) : 0;
+                if (redo)
+                    named_barrier(pair_bar, 32 * HS);        // after the stores above
+                while (redo && h == 0) {
+                    const int row = (warp & 3) * 32 + __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    const int32_t tok = first + (row >> gp_log2);
+                    const int32_t sees = (causal ? min(u.n_k, tok + off + 1) : u.n_k) - skipped;
+                    constexpr int E = D / 32;
+                    float ov[E], rm, rl;
+                    attend_row<T, D>(
+                        p,
+                        static_cast<const unsigned short*>(p.q.data) +
+                            (u.q0 + static_cast<int64_t>(tok)) * p.q.row +
+                            (u.head + (row & (gp - 1))) * p.q.head,
+                        static_cast<const unsigned short*>(p.k.data) +
+                            static_cast<int64_t>(key0_of(u)) * p.k.row + kvh * p.k.head,
+                        static_cast<const unsigned short*>(p.v.data) +
+                            static_cast<int64_t>(key0_of(u)) * p.v.row + kvh * p.v.head,
+                        min(sees, my_kt * BN), scale_log2, ov, rm, rl);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        reinterpret_cast<float*>(&sum->o[(lane * E + e) / 4][row])[(lane * E + e) %
+                                                                                    4] = ov[e];
+                    if (lane == 0)
+                        sum->ml[row] = make_float2(rm, rl);
+                }
+                continue;
+            }
             if (in_place) {
                 redo = leaked(not_finite());
                 rows &= ~redo;
@@ -964,7 +1058,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 const int32_t tok = first + (row >> gp_log2);
                 attend_row_store<T, D>(p, u.q0 + static_cast<int64_t>(tok),
                                        u.head + (row & (gp - 1)), kvh, u.k0,
-                                       CAUSAL ? min(u.n_k, tok + off + 1) : u.n_k, scale_log2);
+                                       causal ? min(u.n_k, tok + off + 1) : u.n_k, scale_log2);
             }
         }
         if (lane == 0)
@@ -991,6 +1085,99 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         tc_fence_after();
         tmem_dealloc_group<CG>(tmem, TMEM_COLS);
     }
+}
+
+// The rows of a unit from its parts, in their order: blockIdx.x counts units
+// and blocks of heads as the parts' kernel does, blockIdx.y blocks of rows; a
+// thread takes four columns of one.
+constexpr int kJoinThreads = 256;
+template <int D> __host__ __device__ constexpr int join_rows() { return kJoinThreads * 4 / D; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+attention_packed_join_kernel(const __grid_constant__ PackedProblem p, int gp_log2, int n_parts)
+{
+    constexpr int CG = Shape<D>::CG, ROWS = join_rows<D>();
+    __shared__ Bounds s_bounds;
+    __shared__ Unit s_unit;
+    const int tid = threadIdx.x;
+    const int tile_tokens = kBM >> gp_log2;
+    const uint32_t blocks = static_cast<uint32_t>(p.n_heads) >> gp_log2;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (tid < 32) {
+        const int tok_log2 = 8 + (CG - 1) - gp_log2;
+        UnitFinder<Shape<D>::BN> finder;
+        finder.init(p, &s_bounds, tok_log2, false, false);
+        const Unit u = finder.find(p, blockIdx.x / blocks, tok_log2);
+        if (tid == 0)
+            s_unit = u;
+    }
+    __syncthreads();
+    const Unit u = s_unit;
+    const int at = blockIdx.y * ROWS, part_tile = at / kBM;      // query tile x CG + rank
+    const int r = at % kBM + tid % ROWS, c4 = tid / ROWS;
+    const int32_t token = (u.tile * 2 * CG + part_tile) * tile_tokens + (r >> gp_log2);
+    if (u.ok <= 0 || token >= u.n_q)
+        return;
+    const auto* const sum = static_cast<const PartSum<D>*>(p.workspace) +
+                            static_cast<int64_t>(blockIdx.x) * n_parts * 2 * CG + part_tile;
+    float m = kNegInf, l = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < n_parts; ++i)
+        m = fmaxf(m, sum[i * 2 * CG].ml[r].x);
+    const float ref = m == kNegInf ? 0.0f : m;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < n_parts; ++i) {
+        const float2 ml = sum[i * 2 * CG].ml[r];
+        const float4 v = sum[i * 2 * CG].o[c4][r];
+        if (ml.x == kNegInf && ml.y == 0.0f)       // saw nothing (what lies there may be anything)
+            continue;
+        const float f = ex2_ftz(ml.x - ref);
+        l += ml.y * f;
+        o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+    }
+    const float inv = 1.0f / l;                    // nothing seen at all: 0 / 0, NaN
+    const int head = static_cast<int>((blockIdx.x % blocks) << gp_log2) + (r & ((1 << gp_log2) - 1));
+    const int64_t row = u.q0 + static_cast<int64_t>(token);
+    uint2 w;
+    w.x = Elem<T>::pack2(o.x * inv, o.y * inv);
+    w.y = Elem<T>::pack2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p.o.data) + row * p.o.row +
+                              static_cast<int64_t>(head) * p.o.head + c4 * 4) = w;
+    if (p.lse && c4 == 0)
+        p.lse[row * p.n_heads + head] =
+            l == 0.0f ? kNegInf : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+// How a call's work is laid out: heads of a group that share a tile's rows (a
+// power of two), units, and the parts that each unit's keys are cut into.
+struct PackedShape {
+    int gp_log2, parts;
+    int64_t units;                                 // of all head blocks; at most
+};
+
+inline PackedShape packed_shape(int64_t n_seqs, int64_t total_q, int64_t total_k, int64_t n_heads,
+                                int64_t n_kv_heads, int cg, int bn, int sm_count)
+{
+    // Query rows of a tile are tokens x heads of one group: as many heads as
+    // the largest power of two that divides the group.
+    const int64_t group = n_heads / n_kv_heads;
+    PackedShape s;
+    s.gp_log2 = 0;
+    while (s.gp_log2 < 5 && group % (2 << s.gp_log2) == 0)
+        ++s.gp_log2;
+    const int64_t tokens = static_cast<int64_t>(2 * cg * kBM) >> s.gp_log2;
+    s.units = (total_q / tokens + n_seqs) * (n_heads >> s.gp_log2);
+    // Few units over long sequences: parts of kPartTiles key tiles or more,
+    // as many as the device holds at once.
+    const int64_t keys = total_k - total_q / 2;    // that the middle query of a prompt sees
+    const int64_t tiles = keys / n_seqs / bn, slots = sm_count / cg;
+    int64_t parts = s.units > 0 ? slots / s.units : 1;
+    parts = parts < tiles / kPartTiles ? parts : tiles / kPartTiles;
+    s.parts = parts < 1 ? 1 : static_cast<int>(parts);
+    return s;
 }
 
 // 3-D tensor map (element, head, row) of a [rows][heads][D] operand: boxes of
@@ -1021,18 +1208,28 @@ inline bool packed_tensor_map(CUtensorMap* map, const Heads& t, int64_t rows, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, bool CAUSAL>
-cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
+template <typename T, int D>
+cudaError_t launch_join(const PackedProblem& p, const PackedShape& sh, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sh.units), 2 * Shape<D>::CG * kBM / join_rows<D>(), 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, 1));
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, attention_packed_join_kernel<T, D>, p,
+                                               sh.gp_log2, sh.parts);
+    note_launch();
+    return err;
+}
+
+template <typename T, int D, int MODE>
+cudaError_t launch_tiles(const PackedProblem& p, const PackedShape& sh, cudaStream_t s)
 {
     using S = Shape<D>;
-    // Query rows of a tile are tokens x heads of one group: as many heads as
-    // the largest power of two that divides the group.
-    const int group = p.n_heads / p.n_kv_heads;
-    int gp_log2 = 0;
-    while (gp_log2 < 5 && group % (2 << gp_log2) == 0)
-        ++gp_log2;
-    const int tile_tokens = kBM >> gp_log2, tokens = 2 * S::CG * tile_tokens;
-    const int64_t units = (p.total_q / tokens + p.n_seqs) * (p.n_heads >> gp_log2);
+    const int gp_log2 = sh.gp_log2, tile_tokens = kBM >> gp_log2;
+    const int64_t units = sh.units * sh.parts;
     if (units * S::CG > 0x7fffffff)
         return cudaErrorNotSupported;
     CUtensorMap mq, mk, mv, mo;
@@ -1043,7 +1240,7 @@ cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
         !packed_tensor_map(&mo, p.o, p.total_q, p.n_heads, D, 1 << gp_log2, 32 >> gp_log2, p.dtype,
                            32))
         return cudaErrorNotSupported;                    // nothing launched
-    auto* kern = attention_packed_kernel<T, D, CAUSAL>;
+    auto* kern = attention_packed_kernel<T, D, MODE>;
     static std::atomic<bool> attr_set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
@@ -1064,8 +1261,11 @@ cudaError_t launch_tiles(const PackedProblem& p, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, S::CG));
     const float scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p, scale_log2, gp_log2);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p, scale_log2, gp_log2,
+                                               sh.parts);
     note_launch();
+    if constexpr (MODE == kParts)
+        return err == cudaSuccess ? launch_join<T, D>(p, sh, s) : err;
     return err;
 }
 
@@ -1089,11 +1289,22 @@ cudaError_t launch_rows(const PackedProblem& p, cudaStream_t s)
     return err;
 }
 
+PackedShape shape_of(int64_t n_seqs, int64_t total_q, int64_t total_k, int64_t n_heads,
+                     int64_t n_kv_heads, int64_t d)
+{
+    return d == 64 ? packed_shape(n_seqs, total_q, total_k, n_heads, n_kv_heads, Shape<64>::CG,
+                                  Shape<64>::BN, sm_count_current())
+                   : packed_shape(n_seqs, total_q, total_k, n_heads, n_kv_heads, Shape<128>::CG,
+                                  Shape<128>::BN, sm_count_current());
+}
+
 template <typename T, int D>
 cudaError_t launch(const PackedProblem& p, cudaStream_t s)
 {
-    const cudaError_t err = p.causal ? launch_tiles<T, D, true>(p, s)
-                                     : launch_tiles<T, D, false>(p, s);
+    const PackedShape sh = shape_of(p.n_seqs, p.total_q, p.total_k, p.n_heads, p.n_kv_heads, D);
+    const cudaError_t err = sh.parts > 1 ? launch_tiles<T, D, kParts>(p, sh, s)
+                            : p.causal   ? launch_tiles<T, D, kCausal>(p, sh, s)
+                                         : launch_tiles<T, D, kFull>(p, sh, s);
     return err == cudaErrorNotSupported ? launch_rows<T, D>(p, s) : err;
 }
 
@@ -1104,6 +1315,17 @@ cudaError_t launch_attention_packed(const PackedProblem& p, cudaStream_t s)
     if (p.dtype == SOFTMAX_BF16)
         return p.head_dim == 64 ? launch<BF16Bits, 64>(p, s) : launch<BF16Bits, 128>(p, s);
     return p.head_dim == 64 ? launch<F16Bits, 64>(p, s) : launch<F16Bits, 128>(p, s);
+}
+
+size_t attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k,
+                                  int64_t n_heads, int64_t n_kv_heads, int64_t head_dim)
+{
+    const PackedShape sh = shape_of(n_seqs, total_q, total_k, n_heads, n_kv_heads, head_dim);
+    if (sh.parts == 1)
+        return 0;
+    const int64_t slots = sh.units * sh.parts * 2;
+    return static_cast<size_t>(head_dim == 64 ? slots * Shape<64>::CG * sizeof(PartSum<64>)
+                                              : slots * Shape<128>::CG * sizeof(PartSum<128>));
 }
 
 unsigned read_error_attention_packed(bool clear)

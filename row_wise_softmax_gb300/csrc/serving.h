@@ -88,8 +88,11 @@ struct PackedProblem {
     int64_t n_seqs, total_q, total_k;
     int32_t n_heads, n_kv_heads, head_dim, causal, dtype;
     float scale;
+    void* workspace;
 };
 cudaError_t launch_attention_packed(const PackedProblem& p, cudaStream_t s);
+size_t attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k,
+                                  int64_t n_heads, int64_t n_kv_heads, int64_t head_dim);
 
 unsigned read_error_kv_append(bool clear);
 unsigned read_error_attention_decode(bool clear);

@@ -309,12 +309,27 @@ int softmax_attention_decode(const softmax_paged_cache_t* cache, const softmax_h
     return status_of(launch_attention_decode(p, static_cast<cudaStream_t>(stream)));
 }
 
+int64_t softmax_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k,
+                                           int64_t n_heads, int64_t n_kv_heads, int64_t head_dim)
+{
+    if (n_seqs < 0 || n_seqs >= kMaxCount || total_q < 0 || total_q > kMaxPacked || total_k < 0 ||
+        total_k > kMaxPacked || n_heads < 1 || n_heads >= kMaxCount || n_kv_heads < 1 ||
+        n_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
+        return -1;
+    if (n_seqs == 0 || total_q == 0)
+        return 0;
+    if (!usable_device())
+        return -1;
+    return static_cast<int64_t>(
+        attention_packed_workspace(n_seqs, total_q, total_k, n_heads, n_kv_heads, head_dim));
+}
+
 int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
                              const softmax_heads_t* v, const softmax_heads_t* o, float* lse,
                              const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
                              int64_t total_q, int64_t total_k, int64_t n_heads,
                              int64_t n_kv_heads, int64_t head_dim, float scale, int causal,
-                             int dtype, void* stream)
+                             int dtype, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (n_seqs < 0 || n_seqs >= kMaxCount || total_q < 0 || total_q > kMaxPacked || total_k < 0 ||
         total_k > kMaxPacked || n_heads < 1 || n_heads >= kMaxCount || n_kv_heads < 1 ||
@@ -335,22 +350,34 @@ int softmax_attention_packed(const softmax_heads_t* q, const softmax_heads_t* k,
         (total_k > 0 && (!apart(*o, total_q, n_heads, *k, total_k, n_kv_heads, d) ||
                          !apart(*o, total_q, n_heads, *v, total_k, n_kv_heads, d))))
         return SOFTMAX_ERR_INVALID_ARG;
-    if (lse) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(lse);
-        const Span sl{a, a + static_cast<uintptr_t>(total_q * n_heads) * 4};
-        if (meet(sl, span_of(*o, total_q, n_heads, d)) || meet(sl, span_of(*q, total_q, n_heads, d)) ||
-            (total_k > 0 && (meet(sl, span_of(*k, total_k, n_kv_heads, d)) ||
-                             meet(sl, span_of(*v, total_k, n_kv_heads, d)))))
-            return SOFTMAX_ERR_INVALID_ARG;
-    }
+    const uintptr_t a_lse = reinterpret_cast<uintptr_t>(lse);
+    const Span sl{a_lse, a_lse + (lse ? static_cast<uintptr_t>(total_q * n_heads) * 4 : 0)};
+    auto meets_operands = [&](const Span& x) {
+        return meet(x, span_of(*o, total_q, n_heads, d)) ||
+               meet(x, span_of(*q, total_q, n_heads, d)) ||
+               (total_k > 0 && (meet(x, span_of(*k, total_k, n_kv_heads, d)) ||
+                                meet(x, span_of(*v, total_k, n_kv_heads, d))));
+    };
+    if (lse && meets_operands(sl))
+        return SOFTMAX_ERR_INVALID_ARG;
     if (!usable_device())
         return SOFTMAX_ERR_UNSUPPORTED;
+    const size_t need =
+        attention_packed_workspace(n_seqs, total_q, total_k, n_heads, n_kv_heads, d);
+    if (need > 0) {
+        if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+            return SOFTMAX_ERR_INVALID_ARG;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(workspace);
+        const Span sw{a, a + need};
+        if (meet(sw, sl) || meets_operands(sw))
+            return SOFTMAX_ERR_INVALID_ARG;
+    }
     const Heads none{nullptr, 0, 0};
     const PackedProblem p{heads(*q), total_k > 0 ? heads(*k) : none,
                           total_k > 0 ? heads(*v) : none, heads(*o), lse, cu_q, cu_k, n_seqs,
                           total_q, total_k, static_cast<int32_t>(n_heads),
                           static_cast<int32_t>(n_kv_heads), static_cast<int32_t>(d), causal,
-                          dtype, scale};
+                          dtype, scale, workspace};
     return status_of(launch_attention_packed(p, static_cast<cudaStream_t>(stream)));
 }
 

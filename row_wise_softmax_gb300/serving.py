@@ -47,8 +47,10 @@ def _lib():
         L.softmax_attention_decode_workspace.argtypes = [i64] * 5
         L.softmax_attention_decode_workspace.restype = i64
         L.softmax_attention_packed.argtypes = [sp, sp, sp, sp, vp, vp, vp, i64, i64, i64, i64, i64,
-                                               i64, cf, ci, ci, vp]
+                                               i64, cf, ci, ci, vp, ctypes.c_size_t, vp]
         L.softmax_attention_packed.restype = ci
+        L.softmax_attention_packed_workspace.argtypes = [i64] * 6
+        L.softmax_attention_packed_workspace.restype = i64
         _declared = L
     return _declared
 
@@ -146,6 +148,12 @@ def _code(name, dtype):
 def _decode_workspace(device, b, h, hk, d, capacity):
     """Workspace bytes of a decode call of these sizes (``device``: current)."""
     return _lib().softmax_attention_decode_workspace(b, h, hk, d, capacity)
+
+
+@functools.lru_cache(maxsize=256)
+def _packed_workspace(device, seqs, n, m, h, hk, d):
+    """Workspace bytes of a packed call of these sizes (``device``: current)."""
+    return _lib().softmax_attention_packed_workspace(seqs, n, m, h, hk, d)
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, positions, seq_ids=None, q=None, q_out=None,
@@ -308,11 +316,14 @@ def attention_packed(q, k, v, cu_q, cu_k=None, scale: float | None = None, causa
     elif out.shape != qshape:
         raise ValueError("attention_packed: out must match q")
     lse = _empty_strided_cuda((n, h), (h, 1), torch.float32) if return_lse else None
+    need = _packed_workspace(device, seqs, n, m, h, hk, d)
+    ws = _empty_strided_cuda((need,), (1,), torch.uint8) if need > 0 else None
     st = (_declared or _lib()).softmax_attention_packed(
         _heads(name, "q", q, dtype, device), _heads(name, "k", k, dtype, device),
         _heads(name, "v", v, dtype, device), _heads(name, "out", out, dtype, device),
         lse.data_ptr() if return_lse else None, cq, ck, seqs, n, m, h, hk, d,
-        d ** -0.5 if scale is None else scale, 1 if causal else 0, code, _raw_stream(device))
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, code,
+        ws.data_ptr() if need > 0 else None, need if need > 0 else 0, _raw_stream(device))
     if st != OK:
         raise SoftmaxError(st, name)
     return (out, lse) if return_lse else out

@@ -19,6 +19,7 @@ import numpy as np
 import pytest
 
 import row_wise_softmax_gb300 as rws
+from row_wise_softmax_gb300.serving import _packed_workspace
 from tests import serving_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -369,6 +370,84 @@ def test_packed_repeated_and_missing_keys():
     o, lse = rws.attention_packed(q, none, none, ints([0, 25, 60]), ints([0, 0, 0]), causal=False,
                                   return_lse=True)
     assert bool(torch.isnan(o).all()) and bool((lse == float("-inf")).all())
+    assert rws.device_status() == rws.OK
+
+
+FEW = [  # few query rows over long sequences, whose keys are cut into parts
+    ([1], [3000], 8, 2, 128, True),
+    ([4, 0, 37], [2500, 600, 1100], 8, 2, 64, True),
+    ([130], [5000], 4, 4, 128, False),
+    ([300], [1300], 2, 1, 64, True),
+    ([70, 9], [40, 6000], 6, 3, 128, True),         # sees nothing; fewer tiles than parts
+    ([513], [1281], 1, 1, 128, True),
+    ([2, 3, 5], [1500, 1409, 4097], 10, 2, 128, False),
+    ([700], [1500], 3, 1, 64, True),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_packed_few_queries(i, dtype):
+    n_q, n_k, h, hk, d, causal = FEW[i]
+    assert _packed_workspace(0, len(n_q), sum(n_q), sum(n_k), h, hk, d) > 0
+    packed_case(n_q, n_k, h, hk, d, causal, dtype, 400 + i, False)
+    packed_case(n_q, n_k, h, hk, d, causal, dtype, 400 + i, False, by=3.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_packed_few_queries_unseen_values(d, bad):
+    """Such values in parts of a sequence, one of them seen by late queries
+    only; out in the place of q; rows behind the last sequence."""
+    g = rng(88)
+    n_q, n_k, h, hk, dtype = 200, 2600, 4, 2, torch.float16
+    q = normal(g, n_q + 5, h, d, dtype=dtype)
+    k, v = (normal(g, n_k + 300, hk, d, dtype=dtype) for _ in range(2))
+    k[n_k:], v[n_k:] = bad, bad                     # behind the sequence
+    v[n_k - 50, 1, 5] = bad                         # seen by its last 50 queries, heads 2 and 3
+    cu_q, cu_k = np.array([0, n_q]), np.array([0, n_k])
+    assert _packed_workspace(0, 1, n_q + 5, n_k + 300, h, hk, d) > 0
+    want, _, mag = ref.packed(f64(q), f64(k), np.where(np.isfinite(f64(v)), f64(v), 0.0), cu_q,
+                              cu_k, d ** -0.5, True)
+    before = f64(q)
+    got = f64(rws.attention_packed(q, k, v, ints(cu_q), ints(cu_k), out=q))
+    assert np.array_equal(got[n_q:], before[n_q:])
+    seen = np.zeros(got.shape, bool)
+    seen[n_q - 50:n_q, 2:, 5] = True
+    seen[n_q:] = True
+    bound = (2.0 ** -11 + 2.0 ** -14) * mag + 2.0 ** -11 * np.abs(want) + 2.0 ** -24 * n_k
+    assert np.all(np.abs(got - want)[~seen] <= bound[~seen])
+    assert not np.any(np.isfinite(got[n_q - 50:n_q, 2:, 5]))
+    assert rws.device_status() == rws.OK
+
+
+def test_packed_few_queries_bad_bounds_and_graph():
+    g = rng(89)
+    h, hk, d, dtype = 8, 2, 128, torch.bfloat16
+    q = normal(g, 12, h, d, dtype=dtype)
+    k, v = (normal(g, 4000, hk, d, dtype=dtype) for _ in range(2))
+    cu_q, cu_k = ints([0, 5, 12]), ints([0, 1900, 4000])
+    want, wl, mag = ref.packed(f64(q), f64(k), f64(v), [0, 5, 12], [0, 1900, 4000], d ** -0.5, True)
+    out = torch.full_like(q, 4.0)
+    rws.attention_packed(q, k, v, cu_q, ints([0, 1900, 4001]), out=out)
+    assert rws.device_status(clear=True) == rws.ERR_DEVICE_INDEX
+    assert bool((out[5:] == 4).all())
+    close(out[:5], None, [w[:5] for w in (want, wl, mag)], dtype, 4000)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        rws.attention_packed(q, k, v, cu_q, cu_k)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            o, lse = rws.attention_packed(q, k, v, cu_q, cu_k, return_lse=True)
+    first = None
+    for _ in range(3):
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        first = o.clone() if first is None else first
+        assert torch.equal(o, first)                # the join's order is fixed
+    close(o, lse, (want, wl, mag), dtype, 4000)
     assert rws.device_status() == rws.OK
 
 

@@ -96,7 +96,7 @@ def packed(lib, q=None, k=None, v=None, o=None, lse=None, cu=32 * MB, ck=33 * MB
     return lib.softmax_attention_packed(
         heads() if q is None else q, heads(4 * MB) if k is None else k,
         heads(5 * MB) if v is None else v, heads(2 * MB) if o is None else o, lse, cu, ck, seqs, tq,
-        tk, h, hk, d, scale, causal, dtype, None)
+        tk, h, hk, d, scale, causal, dtype, None, 0, None)
 
 
 @no_gpu
@@ -120,6 +120,17 @@ def test_packed_refusals(lib):
                   o=heads(MB, row)) == good()
     assert packed(lib, q=heads(MB, row), k=heads(MB + 1024, row), v=heads(MB + 1536, row),
                   o=heads(MB + 1024, row)) == bad
+
+
+@no_gpu
+def test_packed_workspace_of_bad_sizes(lib):
+    f = lib.softmax_attention_packed_workspace
+    assert f(0, 10, 10, 8, 2, 128) == 0 and f(1, 0, 10, 8, 2, 128) == 0
+    for args in ((-1, 10, 10, 8, 2, 128), (1, -1, 10, 8, 2, 128), (1, 10, -1, 8, 2, 128),
+                 (1, 10, 10, 8, 3, 128), (1, 10, 10, 0, 2, 128), (1, 10, 10, 8, 0, 128),
+                 (1, 10, 10, 8, 2, 96), (1, 1 << 31, 10, 8, 2, 128), (1, 10, 1 << 31, 8, 2, 64)):
+        assert f(*args) == -1
+    assert f(1, 10, 10000, 8, 2, 128) == -1                   # no device
 
 
 @no_gpu
