@@ -1,7 +1,47 @@
-// Attention of whole prompts packed one behind the other, grouped heads.
+// Attention of whole prompts packed one behind the other, grouped heads:
+// o_i = sum_j p_ij v_j, p = softmax over a query's visible keys of
+// scale q_i . k_j, with the running softmax over key tiles: for each tile
+//   m' = max(m, max_j s_j), l = l 2^(m - m') + sum_j 2^(s_j - m'),
+//   O = O 2^(m - m') + P V,   s = scale log2(e) q . k,   o = O / l.
 //
-// This form: a warp per (query, head) row, walking the visible keys one at a
-// time with the running (m, l) softmax in fp32.
+//   unit     two query tiles of 128 rows per CTA against all of their keys.
+//            Rows are tokens x heads of one group (as many heads as the
+//            largest power of two in it, at most 32), so that one K/V tile
+//            serves them all.  At D = 128 a cluster of two CTAs shares each
+//            product (cta_group::2: 256 rows, half of K's rows and of V's
+//            columns in each CTA), which halves the shared memory per key and
+//            leaves room for three tiles of 128 keys on the way.  At D = 64 a
+//            CTA's own products are as fast and units half as large.
+//   warps    one copies (tensor maps, a ring of K and V tiles), two issue the
+//            products (one per query tile: what one waits, the other fills),
+//            sixteen compute the softmax: two per row of each tile, 64 keys
+//            each.  S of both tiles goes through one region of tensor memory
+//            in turn, which keeps the tiles out of phase, so that one's
+//            exponentials run beside the other's products; P has its own
+//            columns and is the product's A operand from there, O stays there
+//            (rescaled only when a maximum moves by more than 2^8).
+//   order    CTAs (pairs) stay and take their next unit from the grid itself
+//            by cluster launch control, the units with most key tiles first;
+//            it is found while the one before is computed.  Lengths are on
+//            the device, so a unit is found from the bounds there; the grid
+//            is as large as the sizes allow, units past the last do nothing.
+//   parts    when units are few and sequences long, a unit's keys are cut into
+//            equal parts, computed side by side; a second kernel joins their
+//            (m, l, O) in order.
+//   output   O / l through shared memory by tensor-map copies (a warp's 32 rows x 32
+//            columns), or 16-byte stores where rows of the tile belong to
+//            no query of the sequence.
+//
+// Long prompts are bound by the tensor cores: 4 D operations per visible pair
+// and head.  Measured (bf16, D = 128): 16384 tokens of 16 heads over 2, full
+// 1284 us (1712 TFLOP/s, near the board's power limit), causal 648 us (1697);
+// 4 x 4096 tokens of 16 heads, causal 208 us (1320); 16 ragged prompts up to
+// 4096 of 32 heads over 8, 231 us (1246).  D = 64 is bound by the exponentials
+// and their conversions (two to four products' worth of softmax work per
+// product): 4 x 4096 tokens full 300 us (917 TFLOP/s), causal 175 (785).  A
+// unit's beginning and end cost 2.7 us beside its tiles, which is what short
+// sequences pay: 24 x 500 tokens of 12 heads 37 us (four tiles of 1.4 us a
+// unit, four units a CTA).  Calls of one unit: 90 tokens 9.6 us.
 #include "cluster_ring.cuh"
 #include "common.cuh"
 #include "serving.h"
@@ -9,6 +49,7 @@
 #include "cta_pair.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace rwsm {
 
@@ -158,7 +199,11 @@ constexpr int kHS = 2;                             // warps that share a row of 
 constexpr int kSoftWarps = 2 * 4 * kHS;            // two query tiles of four TMEM lane groups
 constexpr int kStageBytes = 32 * 64;               // a warp's place for 32 x 32 outputs
 
-constexpr int kPartTiles = 2;                      // key tiles of a part, at least
+// Key tiles of a part, at least (of the middle query's keys: a causal prompt
+// without context has half as many).  With 2, 4 and 8: 128 queries of 32 heads
+// over 8 after 1920 keys 18.8, 22.4 and 24.0 us (31.3 whole), 4000 tokens of 2
+// heads 25.0, 30.7 and 30.5 (53.1 whole).
+constexpr int kPartTiles = 2;
 
 constexpr int kPackedThreads = (kSoftWarps + 3) * 32;    // softmax, two MMA warps, copy
 
@@ -175,7 +220,11 @@ struct Unit {
     int32_t q0, n_q, k0, n_k;
     int32_t tile, head;                            // head: first of the block
     int32_t ok;
-    int32_t lo, hi, slot;                          // kParts: its key tiles, its place for the sum
+};
+
+// A part of a unit: its key tiles [lo, hi), its sum's place.
+struct UnitPart : Unit {
+    int32_t lo, hi, slot;
 };
 
 // What the kernel does with a unit: all of its keys, all of them with the
@@ -227,6 +276,15 @@ struct Bounds {
     int32_t q0[kRanked], n_q[kRanked], k0[kRanked], n_k[kRanked];
 };
 
+// Reports sequences with bad bounds, by a warp.
+__device__ __forceinline__ void report_bounds(const PackedProblem& p)
+{
+    int64_t q, nq, k, nk;
+    for (int64_t s = threadIdx.x & 31; s < p.n_seqs; s += 32)
+        if (!sequence_of(p, s, q, nq, k, nk))
+            atomicOr(&g_error_attention_packed, kErrBadIndex);
+}
+
 template <int BN>
 struct UnitFinder {
     Bounds* b;
@@ -236,11 +294,11 @@ struct UnitFinder {
     int64_t at, before;                            // unranked: sequence block, units before it
 
     // Bounds of sequence s into place i (of this lane).
-    __device__ __forceinline__ void lengths(const PackedProblem& p, int64_t s, int i, bool report)
+    __device__ __forceinline__ void lengths(const PackedProblem& p, int64_t s, int i)
     {
         int64_t q = 0, nq = 0, k = 0, nk = 0;
-        if (s < p.n_seqs && !sequence_of(p, s, q, nq, k, nk) && report)
-            atomicOr(&g_error_attention_packed, kErrBadIndex);
+        if (s < p.n_seqs)
+            sequence_of(p, s, q, nq, k, nk);
         b->q0[i] = static_cast<int32_t>(q);
         b->n_q[i] = static_cast<int32_t>(nq);
         b->k0[i] = static_cast<int32_t>(k);
@@ -256,22 +314,18 @@ struct UnitFinder {
         return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
     }
 
-    __device__ void init(const PackedProblem& p, Bounds* bounds, int tok_log2, bool report,
-                         bool by_length)
+    __device__ void init(const PackedProblem& p, Bounds* bounds, int tok_log2, bool by_length)
     {
         const int lane = threadIdx.x & 31;
         b = bounds;
         ranked = by_length && p.n_seqs <= kRanked;
         at = before = 0;
         total = INT64_MAX;
-        if (!ranked) {
-            for (int64_t s = lane; report && s < p.n_seqs; s += 32)
-                lengths(p, s, lane, true);
+        if (!ranked)
             return;
-        }
         int32_t longest = 0;
         for (int i = lane; i < kRanked; i += 32) {
-            lengths(p, i, i, report);
+            lengths(p, i, i);
             if (b->n_q[i] > 0)
                 longest = max(longest, static_cast<int32_t>((b->n_k[i] + BN - 1u) / BN));
         }
@@ -320,7 +374,7 @@ struct UnitFinder {
                 at = before = 0;
             for (; at < p.n_seqs; at += 32) {
                 __syncwarp();
-                lengths(p, at + lane, lane, false);
+                lengths(p, at + lane, lane);
                 __syncwarp();
                 int64_t left = rank - before;
                 int32_t first;
@@ -366,9 +420,10 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ CUtensorMap map_o,
                         const __grid_constant__ PackedProblem p, float scale_log2, int gp_log2,
-                        int n_parts)
+                        int n_parts, int by_length)
 {
     using S = Shape<D>;
+    using Work = std::conditional_t<MODE == kParts, UnitPart, Unit>;
     const bool causal = MODE == kParts ? p.causal != 0 : MODE == kCausal;
     constexpr int CG = S::CG, BN = S::BN, KVS = S::KVS, HS = kHS;
     constexpr bool kBF16 = Elem<T>::kNegInfBits == 0xff80u;
@@ -395,7 +450,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     __shared__ __align__(8) unsigned long long unit_full[2], unit_free[2];
     __shared__ __align__(8) unsigned long long next_full[2], next_free[2];
     __shared__ __align__(16) uint4 s_next[2];                // answers of cluster launch control
-    __shared__ Unit s_unit[2];
+    __shared__ Work s_unit[2];
     __shared__ Bounds s_bounds;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_failed;
@@ -449,6 +504,9 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
     pdl_launch_dependents();
     pdl_wait();
 
+    if (blockIdx.x == 0 && warp == CTRL)
+        report_bounds(p);
+
     auto fail = [&] { *reinterpret_cast<volatile int*>(&s_failed) = 1; };
     auto failed_elsewhere = [&] {
         return __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_failed) != 0) != 0;
@@ -474,12 +532,19 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         return lim <= 0 ? 0 : (lim + BN - 1) / BN;
     };
     // Those that it visits here: all of them, or those of the unit's part.
-    auto tiles_of = [&](const Unit& u, int x) -> int32_t {
+    auto tiles_of = [&](const Work& u, int x) -> int32_t {
         const int32_t n = all_tiles_of(u, x);
-        return MODE != kParts || n <= 0 ? n : max(min(n, u.hi) - u.lo, 0);
+        if constexpr (MODE == kParts)
+            return n <= 0 ? n : max(min(n, u.hi) - u.lo, 0);
+        return n;
     };
-    // First key row of the first of them.
-    auto key0_of = [&](const Unit& u) { return MODE == kParts ? u.k0 + u.lo * BN : u.k0; };
+    // Keys before the first of them, and its first key row.
+    auto skipped_of = [](const Work& u) -> int32_t {
+        if constexpr (MODE == kParts)
+            return u.lo * BN;
+        return 0;
+    };
+    auto key0_of = [&](const Work& u) { return u.k0 + skipped_of(u); };
     // Tile number t, counted through all units, lies in ring slot t % KVS.
     auto slot = [](uint32_t t) { return t % KVS; };
     auto phase = [](uint32_t t) { return (t / KVS) & 1u; };
@@ -496,11 +561,11 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
         const int tok_log2 = 8 + (CG - 1) - gp_log2;
         const uint32_t blocks = static_cast<uint32_t>(p.n_heads) >> gp_log2;
         UnitFinder<BN> finder;
-        finder.init(p, &s_bounds, tok_log2, blockIdx.x == 0, MODE != kParts);
+        finder.init(p, &s_bounds, tok_log2, MODE != kParts && by_length != 0);
         auto find = [&](uint32_t cta) {
             const uint32_t slot = cta / CG, index = MODE == kParts ? slot / n_parts : slot;
             const uint32_t unit = index / blocks;
-            Unit u = finder.find(p, unit, tok_log2);
+            Work u = {finder.find(p, unit, tok_log2)};
             u.head = static_cast<int32_t>((index - unit * blocks) << gp_log2);
             if constexpr (MODE == kParts) {
                 const int64_t n = max(0, max(all_tiles_of(u, 0), all_tiles_of(u, 1)));
@@ -517,7 +582,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                 mbar_arrive_expect_tx(smem_addr(bar), bytes * CG);
             return leader_addr<CG>(smem_addr(bar));
         };
-        Unit u = find(blockIdx.x);
+        Work u = find(blockIdx.x);
         for (uint32_t i = 0; !failed; ++i) {
             if (i >= 2)
                 wait1(&unit_free[i & 1], (i - 2) >> 1);
@@ -539,7 +604,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             }
             const int32_t n_kt = max(tiles_of(u, 0), tiles_of(u, 1));
             const int kvh = u.head / group;
-            Unit next = {};
+            Work next = {};
             if (n_kt > 0) {
                 if (q_uses > 0)
                     wait1(&q_free, q_uses - 1);
@@ -636,7 +701,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             wait1(&unit_full[i & 1], i >> 1);
             if (failed)
                 break;
-            const Unit u = s_unit[i & 1];
+            const Work u = s_unit[i & 1];
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&unit_free[i & 1]));
@@ -748,7 +813,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             named_barrier(1 + x, 128 * HS);
             if (s_stop[i & 1][x])
                 break;
-            const Unit u = s_unit[i & 1];
+            const Work u = s_unit[i & 1];
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&unit_free[i & 1]));
@@ -764,7 +829,7 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
             const int32_t token = first + (r >> gp_log2);    // of the sequence
             // Keys visible to this row, and to every row of the tile (counted
             // from the first of the part).
-            const int32_t skipped = MODE == kParts ? u.lo * BN : 0;
+            const int32_t skipped = skipped_of(u);
             const int32_t limit = (causal ? min(u.n_k, token + off + 1) : u.n_k) - skipped;
             const int32_t limit_all = (causal ? min(u.n_k, first + off + 1) : u.n_k) - skipped;
             float m = kNegInf, l = 0.0f;                     // l: this warp's part of the sum
@@ -1061,8 +1126,8 @@ attention_packed_kernel(const __grid_constant__ CUtensorMap map_q,
                                        causal ? min(u.n_k, tok + off + 1) : u.n_k, scale_log2);
             }
         }
-        if (lane == 0)
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0)                                       // shared memory has been read
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -1108,7 +1173,7 @@ attention_packed_join_kernel(const __grid_constant__ PackedProblem p, int gp_log
     if (tid < 32) {
         const int tok_log2 = 8 + (CG - 1) - gp_log2;
         UnitFinder<Shape<D>::BN> finder;
-        finder.init(p, &s_bounds, tok_log2, false, false);
+        finder.init(p, &s_bounds, tok_log2, false);
         const Unit u = finder.find(p, blockIdx.x / blocks, tok_log2);
         if (tid == 0)
             s_unit = u;
@@ -1261,8 +1326,11 @@ cudaError_t launch_tiles(const PackedProblem& p, const PackedShape& sh, cudaStre
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, S::CG));
     const float scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
+    // Units that all run at once may come in any order: the sequences' own
+    // needs no ranking (90 tokens: 10.4 -> 9.7 us).
+    const int by_length = units > sm_count_current() / S::CG;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p, scale_log2, gp_log2,
-                                               sh.parts);
+                                               sh.parts, by_length);
     note_launch();
     if constexpr (MODE == kParts)
         return err == cudaSuccess ? launch_join<T, D>(p, sh, s) : err;
