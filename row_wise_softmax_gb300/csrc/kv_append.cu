@@ -13,7 +13,10 @@
 //
 // Bound by bytes: every element is read and written once (16-byte vectors),
 // against a few multiply-adds each.  A CTA computes its tokens' cosines and
-// sines once, into shared memory, for all of their heads.
+// sines once, into shared memory, for all of their heads.  Measured (32 query
+// heads, 8 key/value heads of 128, bf16): 16001 tokens 64.7 us with inputs not
+// in L2 (6.1 TB/s, a plain copy runs at 6.7); 256 tokens 4.1 us and 8 tokens 3.2,
+// which is the launch, the index reads one behind the other, and the angles.
 #include "common.cuh"
 #include "serving.h"
 
@@ -195,6 +198,10 @@ kv_append_kernel(const AppendProblem p)
 template <typename T, int D>
 cudaError_t launch(const AppendProblem& p, cudaStream_t s)
 {
+    // A CTA per token spreads few tokens wide, one per four computes the angles
+    // of many with every thread at work: 8 tokens 3.2 against 5.4 us, 256 4.1
+    // against 5.6, 1024 8.2 against 8.8, 2048 12.5 against 13.5, 4096 26.3
+    // against 22.0, 16001 96 against 70 (outputs in L2).
     constexpr int TT = 4;
     const bool few = p.n_tokens <= 1024;
     auto* kern = few ? kv_append_kernel<T, D, 1> : kv_append_kernel<T, D, TT>;
