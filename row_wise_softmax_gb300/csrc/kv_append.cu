@@ -14,8 +14,8 @@
 // Bound by bytes: every element is read and written once (16-byte vectors),
 // against a few multiply-adds each.  A CTA computes its tokens' cosines and
 // sines once, into shared memory, for all of their heads.  Measured (32 query
-// heads, 8 key/value heads of 128, bf16): 16001 tokens 64.7 us with inputs not
-// in L2 (6.1 TB/s, a plain copy runs at 6.7); 256 tokens 4.1 us and 8 tokens 3.2,
+// heads, 8 key/value heads of 128, bf16): 16001 tokens 64.2 us with inputs not
+// in L2 (6.1 TB/s, a plain copy runs at 6.7); 256 tokens 4.2 us and 8 tokens 3.1,
 // which is the launch, the index reads one behind the other, and the angles.
 #include "common.cuh"
 #include "serving.h"
@@ -57,6 +57,14 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
     return w;
 }
 
+// (a, b) turned by the angle of cosine c and sine s.
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s)
+{
+    const float x = a, y = b;
+    a = x * c - y * s;
+    b = x * s + y * c;
+}
+
 // TT tokens per CTA.  A work unit is two 16-byte vectors of one head: with
 // D / 16 units to a head, unit u holds vectors (u, u + rot / 16) of the
 // rotated part (halves), or (2u, 2u + 1) (interleaved, and past the rotated
@@ -66,8 +74,11 @@ __global__ void __launch_bounds__(kThreads)
 kv_append_kernel(const AppendProblem p)
 {
     constexpr int U = D / 16;
-    constexpr int kBatch = TT == 1 ? 1 : 2;        // units that a thread has under way
-    __shared__ float2 turn[TT][kMaxHalf];
+    // Units that a thread has under way: with few CTAs on the device two keep
+    // more bytes in flight (1024 tokens 8.5 -> 7.8 us), with many the registers
+    // cost more than they bring (16001 tokens 64 -> 73 us).
+    constexpr int kBatch = TT == 1 ? 2 : 1;
+    __shared__ __align__(16) float2 turn[TT][kMaxHalf];
     __shared__ int64_t k_at[TT], v_at[TT];         // cache element of the token, < 0: none
     __shared__ int32_t pos_of[TT];
     const int tid = threadIdx.x;
@@ -77,6 +88,38 @@ kv_append_kernel(const AppendProblem p)
 
     pdl_launch_dependents();
     pdl_wait();
+    const int nq = p.q.data ? p.n_heads : 0, nk = p.cache.n_kv_heads;
+    const int per_token = (nq + 2 * nk) * U, units = per_token * tokens;
+    // A thread's units, kBatch at a time: all of their loads are under way
+    // before the first is used, those of the first batch before the tokens'
+    // places and angles are known (a token that turns out to be padding is
+    // read in vain).
+    uint4 w0[kBatch], w1[kBatch];
+    auto place = [&](int i, int& t, int& r, int& u) {
+        t = TT == 1 ? 0 : i / per_token;
+        r = (i - t * per_token) / U;
+        u = i % U;
+    };
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = i0 + b * kThreads;
+            if (i >= units)
+                continue;
+            int t, r, u;
+            place(i, t, r, u);
+            // Which tensor this head row belongs to.
+            const Heads& x = r < nq ? p.q : r < nq + nk ? p.k : p.v;
+            const int head = r < nq ? r : r < nq + nk ? r - nq : r - nq - nk;
+            const unsigned short* src = static_cast<const unsigned short*>(x.data) +
+                                        (t0 + t) * x.row + head * x.head;
+            const bool apart = r < nq + nk && u * 16 < p.rot_dim && !p.interleaved;
+            w0[b] = *reinterpret_cast<const uint4*>(src + (apart ? u : 2 * u) * 8);
+            w1[b] = *reinterpret_cast<const uint4*>(
+                src + (apart ? u + p.rot_dim / 16 : 2 * u + 1) * 8);
+        }
+    };
+    load(tid);
     if (tid < tokens) {
         const int32_t pos = p.positions[t0 + tid];
         pos_of[tid] = pos;
@@ -110,87 +153,62 @@ kv_append_kernel(const AppendProblem p)
     }
     __syncthreads();
 
-    const int nq = p.q.data ? p.n_heads : 0, nk = p.cache.n_kv_heads;
-    const int per_token = (nq + 2 * nk) * U, units = per_token * tokens;
-    // kBatch units at a time: all of their loads are under way before the
-    // first is used.
     for (int i0 = tid; i0 < units; i0 += kThreads * kBatch) {
-        unsigned short* dst[kBatch];               // null: nothing to do
-        uint4 w0[kBatch], w1[kBatch];
-        int c0[kBatch], c1[kBatch], turn_at[kBatch];   // turn_at < 0: copied as it is
+        if (i0 != tid)
+            load(i0);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int i = i0 + b * kThreads;
-            dst[b] = nullptr;
             if (i >= units)
                 continue;
-            const int t = TT == 1 ? 0 : i / per_token, r = (i - t * per_token) / U, u = i % U;
+            int t, r, u;
+            place(i, t, r, u);
             if (pos_of[t] < 0)
                 continue;
-            // Which tensor this head row belongs to.
-            const int64_t token = t0 + t;
-            const unsigned short* src;
+            unsigned short* dst;
             if (r < nq) {
-                src = static_cast<const unsigned short*>(p.q.data) + token * p.q.row + r * p.q.head;
-                dst[b] = static_cast<unsigned short*>(p.q_out.data) + token * p.q_out.row +
-                         r * p.q_out.head;
+                dst = static_cast<unsigned short*>(p.q_out.data) + (t0 + t) * p.q_out.row +
+                      r * p.q_out.head;
             } else if (r < nq + nk) {
                 if (k_at[t] < 0)
                     continue;
-                src = static_cast<const unsigned short*>(p.k.data) + token * p.k.row +
-                      (r - nq) * p.k.head;
-                dst[b] = static_cast<unsigned short*>(p.cache.k) + k_at[t] +
-                         (r - nq) * p.cache.k_head;
+                dst = static_cast<unsigned short*>(p.cache.k) + k_at[t] +
+                      (r - nq) * p.cache.k_head;
             } else {
                 if (v_at[t] < 0)
                     continue;
-                src = static_cast<const unsigned short*>(p.v.data) + token * p.v.row +
-                      (r - nq - nk) * p.v.head;
-                dst[b] = static_cast<unsigned short*>(p.cache.v) + v_at[t] +
-                         (r - nq - nk) * p.cache.v_head;
+                dst = static_cast<unsigned short*>(p.cache.v) + v_at[t] +
+                      (r - nq - nk) * p.cache.v_head;
             }
             const bool turns = r < nq + nk && u * 16 < p.rot_dim;
             const bool apart = turns && !p.interleaved;
-            turn_at[b] = turns ? t * kMaxHalf + u * 8 : -1;
-            c0[b] = apart ? u : 2 * u;
-            c1[b] = apart ? u + p.rot_dim / 16 : 2 * u + 1;
-            w0[b] = *reinterpret_cast<const uint4*>(src + c0[b] * 8);
-            w1[b] = *reinterpret_cast<const uint4*>(src + c1[b] * 8);
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (!dst[b])
-                continue;
-            if (turn_at[b] >= 0) {
+            if (turns) {
                 float x[8], y[8];
                 unpack8<T>(w0[b], x);
                 unpack8<T>(w1[b], y);
-                const float2* cs = &turn[0][0] + turn_at[b];
+                const float4* cs = reinterpret_cast<const float4*>(&turn[t][u * 8]);
                 if (p.interleaved) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = cs[j], g = cs[j + 4];
-                        const float x0 = x[2 * j], x1 = x[2 * j + 1];
-                        const float y0 = y[2 * j], y1 = y[2 * j + 1];
-                        x[2 * j] = x0 * f.x - x1 * f.y;
-                        x[2 * j + 1] = x0 * f.y + x1 * f.x;
-                        y[2 * j] = y0 * g.x - y1 * g.y;
-                        y[2 * j + 1] = y0 * g.y + y1 * g.x;
+                    for (int j = 0; j < 4; j += 2) {
+                        const float4 f = cs[j / 2], g = cs[j / 2 + 2];
+                        rotate(x[2 * j], x[2 * j + 1], f.x, f.y);
+                        rotate(x[2 * j + 2], x[2 * j + 3], f.z, f.w);
+                        rotate(y[2 * j], y[2 * j + 1], g.x, g.y);
+                        rotate(y[2 * j + 2], y[2 * j + 3], g.z, g.w);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = cs[j];
-                        const float x0 = x[j], y0 = y[j];
-                        x[j] = x0 * f.x - y0 * f.y;
-                        y[j] = x0 * f.y + y0 * f.x;
+                    for (int j = 0; j < 8; j += 2) {
+                        const float4 f = cs[j / 2];
+                        rotate(x[j], y[j], f.x, f.y);
+                        rotate(x[j + 1], y[j + 1], f.z, f.w);
                     }
                 }
                 w0[b] = pack8<T>(x);
                 w1[b] = pack8<T>(y);
             }
-            *reinterpret_cast<uint4*>(dst[b] + c0[b] * 8) = w0[b];
-            *reinterpret_cast<uint4*>(dst[b] + c1[b] * 8) = w1[b];
+            *reinterpret_cast<uint4*>(dst + (apart ? u : 2 * u) * 8) = w0[b];
+            *reinterpret_cast<uint4*>(dst + (apart ? u + p.rot_dim / 16 : 2 * u + 1) * 8) = w1[b];
         }
     }
 }
@@ -198,14 +216,17 @@ kv_append_kernel(const AppendProblem p)
 template <typename T, int D>
 cudaError_t launch(const AppendProblem& p, cudaStream_t s)
 {
-    // A CTA per token spreads few tokens wide, one per four computes the angles
-    // of many with every thread at work: 8 tokens 3.2 against 5.4 us, 256 4.1
-    // against 5.6, 1024 8.2 against 8.8, 2048 12.5 against 13.5, 4096 26.3
-    // against 22.0, 16001 96 against 70 (outputs in L2).
-    constexpr int TT = 4;
-    const bool few = p.n_tokens <= 1024;
-    auto* kern = few ? kv_append_kernel<T, D, 1> : kv_append_kernel<T, D, TT>;
-    const int64_t grid = few ? p.n_tokens : (p.n_tokens + TT - 1) / TT;
+    // A CTA per token spreads few tokens wide (8 tokens 3.1 us; one per four
+    // 5.4), one per two or four computes the angles of many with every thread
+    // at work and ends in fewer waves: with 1, 2 and 4 tokens to a CTA, 2048
+    // tokens take 13.9, 11.6 and 15.0 us, 4096 28.0, 20.8 and 22.5, 16001 95,
+    // 67 and 64.
+    const int64_t n = p.n_tokens;
+    const int tt = n <= 1024 ? 1 : n <= 4096 ? 2 : 4;
+    auto* kern = tt == 1   ? kv_append_kernel<T, D, 1>
+                 : tt == 2 ? kv_append_kernel<T, D, 2>
+                           : kv_append_kernel<T, D, 4>;
+    const int64_t grid = (n + tt - 1) / tt;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);

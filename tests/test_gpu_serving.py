@@ -553,6 +553,8 @@ APPEND = [  # tokens, heads, kv_heads, head_dim, rot_dim, interleaved, page
     (5, 3, 3, 128, 0, False, 16),
     (1500, 8, 2, 64, 64, True, 16),
     (1201, 3, 1, 128, 96, False, 32),
+    (5003, 3, 1, 128, 64, True, 16),
+    (4098, 4, 2, 64, 64, False, 8),
 ]
 
 
