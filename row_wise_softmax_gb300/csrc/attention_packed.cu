@@ -36,10 +36,11 @@
 // and head.  Measured (bf16, D = 128): 16384 tokens of 16 heads over 2, full
 // 1284 us (1712 TFLOP/s, near the board's power limit), causal 648 us (1697);
 // 4 x 4096 tokens of 16 heads, causal 208 us (1320); 16 ragged prompts up to
-// 4096 of 32 heads over 8, 231 us (1246).  D = 64 is bound by the exponentials
-// and their conversions (two to four products' worth of softmax work per
-// product): 4 x 4096 tokens full 300 us (917 TFLOP/s), causal 175 (785).  A
-// unit's beginning and end cost 2.7 us beside its tiles, which is what short
+// 4096 of 32 heads over 8, 231 us (1246).  D = 64 has half the products per
+// exponential: 4 x 4096 tokens full 300 us (917 TFLOP/s), causal 175 (785); the
+// tensor pipe is 21% and the exponential pipe 21% busy at 24 x 500 tokens, and
+// what warps wait for is each other (a tile's maxima, its product).  A unit's
+// beginning and end cost 2.7 us beside its tiles, which is what short
 // sequences pay: 24 x 500 tokens of 12 heads 37 us (four tiles of 1.4 us a
 // unit, four units a CTA).  Calls of one unit: 90 tokens 9.6 us.
 #include "cluster_ring.cuh"
