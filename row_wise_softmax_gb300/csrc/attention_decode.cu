@@ -19,8 +19,8 @@
 //   warp     16 tokens (32 at D = 64) of each tile, on its own: its K and V
 //            rows arrive by cp.async in its own ring of stages (no CTA barrier
 //            in the walk), rows past the length as zeros.  Pages are of any
-//            size, so rows are fetched one by one by their places; a tensor
-//            map would need a page size.  S = Q K^T by mma.sync m16n8k16
+//            size and may end inside a tile, so rows are fetched one by one by
+//            their places.  S = Q K^T by mma.sync m16n8k16
 //            with the group's heads as the 16 rows; the scores' accumulator
 //            layout is the A operand of P V.
 //
